@@ -30,7 +30,8 @@
  *     on `stream` (a cudaStream_t; NULL = the legacy default stream) and returns.
  *   - Matrices are row-major. `ld_*` is the distance in ELEMENTS between consecutive rows.
  *     Rotary tensors are contiguous [B, S, H, D]; tables are contiguous fp32 [S, D/2].
- *   - `dt` selects the element type of x, y, dy, dx, w, b, q, k (GN_F32 or GN_BF16).
+ *   - `dt` selects the element type of x, y, dy, dx, w, b, q, k (GN_F32 or GN_BF16); the codes of
+ *     the 8-bit calls are e4m3 bytes.
  *     Saved statistics (inv_rms, mean, rstd), weight gradients and tables are always fp32.
  *   - Arithmetic is fp32 with one round-to-nearest-even per stored bf16 element.
  *   - Arguments are checked before anything is enqueued. A check that fails returns its
@@ -78,6 +79,9 @@ typedef enum { GN_F32 = 0, GN_BF16 = 1 } gn_dtype;
 
 /* epilogue applied to z = normalized * weight (+ bias) before the store */
 typedef enum { GN_EPI_NONE = 0, GN_EPI_GELU_TANH = 1, GN_EPI_SILU = 2 } gn_epilogue;
+
+/* the blocks of values that share one scale in gn_quant_fp8: 128 along a row, or 128 x 128 */
+typedef enum { GN_FP8_VEC = 0, GN_FP8_TILE = 1 } gn_fp8_block;
 
 /* the normalization in front of the fused linear layer (GN_NORM_NONE: a plain linear layer) */
 typedef enum { GN_NORM_RMS = 0, GN_NORM_LN = 1, GN_NORM_NONE = 2 } gn_norm;
@@ -311,6 +315,97 @@ gn_status gn_act_grad(const void* z, const void* dy, void* dz, int64_t n, gn_epi
  * y may alias z (in place).
  * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE (n < 0), GN_ERR_NULL, GN_ERR_ALIGN, GN_ERR_CUDA. */
 gn_status gn_act_fwd(const void* z, void* y, int64_t n, gn_epilogue epi, gn_dtype dt, void* stream);
+
+/* ---------------------------------------------------------------- GroupNorm, channels last
+ * x [N, S, C]: N images of S positions (a flattened picture or video), C channels, row (n, s) at
+ * (n S + s) ld_x elements. The channels form G groups of P = C / G consecutive ones; a group's
+ * statistics run over its S P values of one image:
+ *   mu = mean(x);  var = mean((x - mu)^2)  (biased);  s = 1 / sqrt(var + eps)
+ *   y = epi((x - mu) s w_c + b_c)
+ *   mean[n, group] = mu, rstd[n, group] = s                (fp32 [N, G]; each may be NULL)
+ * w, b: dt [C]; w == NULL means 1, b == NULL means 0. x, y: 16-byte aligned, row strides of whole
+ * 16 bytes; any C, G dividing C. y may alias x when ld_y == ld_x (in place).
+ * ws: device scratch of gn_groupnorm_fwd_workspace(N, S, C, G, dt) bytes, 16-byte aligned, owned by
+ * the caller, contents ignored on entry; calls that overlap on the GPU need one each. The size is
+ * that of the current device. Every sum runs in a fixed order: the same bits on every run.
+ * N == 0 or S == 0: nothing is launched and no statistic is written.
+ * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE (sizes, G not dividing C, strides), GN_ERR_NULL, GN_ERR_ALIGN,
+ * GN_ERR_WORKSPACE, GN_ERR_CUDA. */
+size_t gn_groupnorm_fwd_workspace(int64_t N, int64_t S, int64_t C, int64_t G, gn_dtype dt);
+gn_status gn_groupnorm_fwd(const void* x, const void* w, const void* b, void* y, float* mean,
+                           float* rstd, void* ws, size_t ws_bytes, int64_t N, int64_t S, int64_t C,
+                           int64_t G, int64_t ld_x, int64_t ld_y, float eps, gn_epilogue epi,
+                           gn_dtype dt, void* stream);
+
+/* Backward of gn_groupnorm_fwd from the saved mean and rstd (fp32 [N, G], required):
+ *   xhat = (x - mu) s, z = xhat w + b, g = dy * epi'(z)
+ *   dx = s (g w_c - mean(g w) - xhat mean(g w xhat))       (means over the group's S P values)
+ *   dw[c] = sum over images and positions of g xhat,  db[c] = sum of g
+ *                                                          (fp32 [C]; each may be NULL)
+ * dx may alias dy. ws: gn_groupnorm_bwd_workspace bytes, as above (needed in every case). */
+size_t gn_groupnorm_bwd_workspace(int64_t N, int64_t S, int64_t C, int64_t G, gn_dtype dt);
+gn_status gn_groupnorm_bwd(const void* x, const void* w, const void* b, const float* mean,
+                           const float* rstd, const void* dy, void* dx, float* dw, float* db, void* ws,
+                           size_t ws_bytes, int64_t N, int64_t S, int64_t C, int64_t G, int64_t ld_x,
+                           int64_t ld_dy, int64_t ld_dx, gn_epilogue epi, gn_dtype dt, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit operands, one scale per 128 values
+ * A block of 128 values v (shorter at the end of a row) is held as e4m3 codes q and an fp32 scale s
+ * with v ~ q s:
+ *   s = max(max|v|, 2^-110) / 448,   q = e4m3(v / s)   (the fp32 quotient, nearest even)
+ * A block that holds a NaN or an infinity gets the scale NaN and NaN codes.
+ * Codes are bytes (e4m3, no infinities), their rows 16-byte aligned (base and stride); scales are
+ * fp32 matrices with one column per block. Values are formed in fp32 and rounded only to codes. */
+
+/* Norm + activation + quantisation of the rows of x [rows, hidden] (dt), blocks along the row: the
+ * operand A of gn_linear_fp8 behind a normalization.
+ *   v = epi(norm(x));  GN_NORM_RMS: x r g' (g' = g or 1 + g with gemma), GN_NORM_LN:
+ *   (x - mu) r g + beta, GN_NORM_NONE: x
+ * g, beta: dt [hidden] (NULL = ones / zeros; beta is read by GN_NORM_LN only, both are ignored by
+ * GN_NORM_NONE). q: codes [rows, hidden], ld_q; scale: [rows, ceil(hidden / 128)], ld_s. mean
+ * (GN_NORM_LN), rstd: fp32 [rows], each may be NULL.
+ * Limit: hidden <= 16384 (bf16) / 8192 (fp32), else GN_ERR_UNSUPPORTED. rows <= 2^31 - 1.
+ * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE, GN_ERR_UNSUPPORTED, GN_ERR_NULL, GN_ERR_ALIGN, GN_ERR_CUDA. */
+gn_status gn_norm_quant_fp8(const void* x, const void* g, const void* beta, void* q, float* scale,
+                            float* mean, float* rstd, int64_t rows, int64_t hidden, int64_t ld_x,
+                            int64_t ld_q, int64_t ld_s, float eps, gn_norm norm, int gemma,
+                            gn_epilogue epi, gn_dtype dt, void* stream);
+
+/* Quantisation of a matrix v [rows, cols], by rows (q, scale) and / or transposed (qt, scale_t), in
+ * one pass: v = x, or with dy given v = dy * epi'(x) (the gradient of a pre-activation x from the
+ * gradient dy of its activation).
+ *   GN_FP8_VEC : q [rows, cols] in blocks of 128 along a row, scale [rows, ceil(cols / 128)];
+ *                qt [cols, rows] in blocks of 128 along the rows of v, scale_t [cols, ceil(rows / 128)]
+ *   GN_FP8_TILE: blocks of 128 x 128; scale [ceil(rows / 128), ceil(cols / 128)], scale_t its
+ *                transpose, qt the transpose of q (a weight; dy must be NULL)
+ * q or qt may be NULL (not written). db: fp32 [cols], may be NULL: the column sums of v (a bias
+ * gradient; fp32 in a fixed order), which needs ws of gn_quant_fp8_workspace(rows, cols) bytes, 16-byte
+ * aligned, contents ignored. rows <= 8388480.
+ * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE, GN_ERR_UNSUPPORTED (an epilogue without dy; dy with tiles),
+ * GN_ERR_NULL, GN_ERR_ALIGN, GN_ERR_WORKSPACE, GN_ERR_CUDA. rows == 0: nothing is launched, db is
+ * set to zero. */
+size_t gn_quant_fp8_workspace(int64_t rows, int64_t cols);
+gn_status gn_quant_fp8(const void* x, const void* dy, void* q, float* scale, void* qt, float* scale_t,
+                       float* db, void* ws, size_t ws_bytes, int64_t rows, int64_t cols, int64_t ld_x,
+                       int64_t ld_dy, int64_t ld_q, int64_t ld_s, int64_t ld_qt, int64_t ld_st,
+                       gn_fp8_block block, gn_epilogue epi, gn_dtype dt, void* stream);
+
+/* y [M, N] = act(A B^T + d) for 8-bit A [M, K] and B [N, K] (codes, K contiguous) with one scale
+ * for each 128 values of the contraction:
+ *   y[m, n] = act( sum_b sa[m, b] sb[n / b_rows, b] sum_{k in block b} A[m, k] B[n, k] + d[n] )
+ * sa [M, ceil(K / 128)]; sb [ceil(N / b_rows), ceil(K / 128)] with b_rows 128 (a weight in 128 x 128
+ * blocks) or 1 (a scale per row). d: fp32 [N], may be NULL = 0. out GN_BF16: y bf16. out GN_F32: y
+ * fp32, no activation; accumulate != 0: y += A B^T + d (GN_F32 only). Block products and sums are
+ * fp32. The gradients of the layer are the same product on gn_quant_fp8's operands: dx = dz W
+ * (A = dz by rows, B = W transposed), dW = dz^T x (A = dz transposed, B = x transposed, b_rows 1).
+ * Any M, N, K >= 1; A, B, y, d 16-byte aligned, row strides ld_a, ld_b, ld_y of whole 16 bytes.
+ * M <= 8388480.
+ * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE, GN_ERR_UNSUPPORTED (activation with GN_F32, accumulate with
+ * GN_BF16), GN_ERR_NULL, GN_ERR_ALIGN, GN_ERR_CUDA. M == 0 or N == 0: nothing is launched. */
+gn_status gn_linear_fp8(const void* A, const float* sa, const void* B, const float* sb, const float* d,
+                        void* y, int64_t M, int64_t N, int64_t K, int64_t ld_a, int64_t ld_sa,
+                        int64_t ld_b, int64_t ld_sb, int64_t ld_y, int64_t b_rows, int accumulate,
+                        gn_epilogue epi, gn_dtype out, void* stream);
 
 /* ---------------------------------------------------------------- runtime queries
  * Number of kernels this process has launched through libgn (all devices, all threads). */

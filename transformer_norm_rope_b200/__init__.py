@@ -15,6 +15,7 @@ Build it with ``python -m transformer_norm_rope_b200._build``.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -25,6 +26,7 @@ GN_OK, GN_ERR_NULL, GN_ERR_SHAPE, GN_ERR_ALIGN, GN_ERR_DTYPE, GN_ERR_WORKSPACE, 
 GN_F32, GN_BF16 = 0, 1
 GN_EPI_NONE, GN_EPI_GELU_TANH, GN_EPI_SILU = 0, 1, 2
 GN_NORM_RMS, GN_NORM_LN, GN_NORM_NONE = 0, 1, 2
+GN_FP8_VEC, GN_FP8_TILE = 0, 1
 GN_DEVERR_WAIT_TIMEOUT = 1
 EPILOGUES = {"none": GN_EPI_NONE, "gelu_tanh": GN_EPI_GELU_TANH, "silu": GN_EPI_SILU}
 
@@ -61,6 +63,19 @@ SIGNATURES = {
     "gn_colsum_bf16": (_st, [_vp, _vp, _vp, _sz, _i64, _i64, _i64, _int, _int, _vp]),
     "gn_act_grad": (_st, [_vp, _vp, _vp, _i64, _int, _int, _vp]),
     "gn_act_fwd": (_st, [_vp, _vp, _i64, _int, _int, _vp]),
+    "gn_groupnorm_fwd_workspace": (_sz, [_i64, _i64, _i64, _i64, _int]),
+    "gn_groupnorm_fwd": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _int,
+                               _int, _vp]),
+    "gn_groupnorm_bwd_workspace": (_sz, [_i64, _i64, _i64, _i64, _int]),
+    "gn_groupnorm_bwd": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _i64, _i64, _i64,
+                               _i64, _i64, _int, _int, _vp]),
+    "gn_norm_quant_fp8": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _f32, _int, _int, _int,
+                                _int, _vp]),
+    "gn_quant_fp8_workspace": (_sz, [_i64, _i64]),
+    "gn_quant_fp8": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64,
+                           _int, _int, _int, _vp]),
+    "gn_linear_fp8": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _int,
+                            _int, _int, _vp]),
     "gn_launch_count": (C.c_uint64, []),
     "gn_device_error": (_st, [C.POINTER(C.c_uint), _int]),
     "gn_selftest_wait_timeout": (_st, [C.c_uint32, _vp]),
@@ -494,6 +509,207 @@ def colsum_bf16(src, out, accumulate=False, ws=None, stream=None):
     check(gn_colsum_bf16(_ptr(src), _ptr(out), _ptr(ws), ws.numel(), rows, cols, ld, int(accumulate), _dt(src),
                          _stream(stream)), "gn_colsum_bf16")
     return out
+
+
+def _placed(f):
+    """Runs a helper with its first tensor's device current and its outputs and workspace allocated
+    for the stream that the call uses: memory freed on one stream is otherwise handed out again
+    while a kernel on another still works in it."""
+
+    @functools.wraps(f)
+    def call(x, *args, stream=None, **kwargs):
+        torch = _torch()
+        if not x.is_cuda or (stream is None and x.device.index == torch.cuda.current_device()):
+            return f(x, *args, stream=stream, **kwargs)
+        if stream is None:
+            with torch.cuda.device(x.device):
+                return f(x, *args, **kwargs)
+        if stream.device != x.device:
+            raise ValueError(f"the stream is on {stream.device}, the operands on {x.device}")
+        with torch.cuda.stream(stream):
+            return f(x, *args, stream=stream, **kwargs)
+
+    return call
+
+
+def _rows16(x, name="x", like=None, dtype=None):
+    """_rows, with the row stride of a matrix of one row or none (which nothing steps by) taken as
+    its width in whole 16 bytes."""
+    rows, hidden, ld = _rows(x, name, like=like, dtype=dtype)
+    if rows <= 1:
+        es = x.element_size()
+        ld = (hidden * es + 15) // 16 * 16 // es
+    return rows, hidden, ld
+
+
+def _images(x, name="x", like=None, dtype=None):
+    """(N, S, C, ld) of a channels-last tensor [N, ..., C] whose positions form one strided matrix."""
+    if x.dim() < 2:
+        raise ValueError(f"{name} must be [N, ..., C]")
+    rows, C, ld = _rows16(x, name, like=like, dtype=dtype)
+    N = x.shape[0]
+    S = 1
+    for n in x.shape[1:-1]:
+        S *= n
+    return N, S, C, ld
+
+
+@_placed
+def groupnorm_fwd(x, groups, w=None, b=None, eps=1e-5, epilogue="none", out=None, save_stats=True, stream=None):
+    """GroupNorm of channels-last images x [N, ..., C] with an activation:
+    y = epi((x - mean) * rstd * w + b), statistics over each image's groups of C / groups consecutive
+    channels -> (y, mean [N, groups], rstd [N, groups]) (statistics fp32, or None)."""
+    torch = _torch()
+    N, S, Cn, ld = _images(x)
+    _need(w, "w", like=x, shape=(Cn,), dtype=x.dtype, optional=True)
+    _need(b, "b", like=x, shape=(Cn,), dtype=x.dtype, optional=True)
+    y = empty_rows(x.shape, x.dtype, x.device) if out is None else out
+    _need(y, "out", like=x, shape=x.shape, contiguous=False)
+    _, _, _, ldy = _images(y, "out", like=x, dtype=x.dtype)
+    mk = (lambda: torch.empty((N, groups), dtype=torch.float32, device=x.device))
+    mu, rs = (mk(), mk()) if save_stats else (None, None)
+    nws = gn_groupnorm_fwd_workspace(N, S, Cn, groups, _dt(x))
+    ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=x.device)
+    check(gn_groupnorm_fwd(_ptr(x), _ptr(w), _ptr(b), _ptr(y), _ptr(mu), _ptr(rs), _ptr(ws), nws, N, S, Cn, groups, ld,
+                           ldy, eps, _epi(epilogue), _dt(x), _stream(stream)), "gn_groupnorm_fwd")
+    return y, mu, rs
+
+
+@_placed
+def groupnorm_bwd(x, groups, w, b, mean, rstd, dy, epilogue="none", want_wgrad=True, stream=None):
+    """Backward of groupnorm_fwd from its saved statistics -> (dx, dw, db) (dw, db fp32 or None)."""
+    torch = _torch()
+    N, S, Cn, ld = _images(x)
+    _need(w, "w", like=x, shape=(Cn,), dtype=x.dtype, optional=True)
+    _need(b, "b", like=x, shape=(Cn,), dtype=x.dtype, optional=True)
+    _need(mean, "mean", like=x, shape=(N, groups), dtype=torch.float32)
+    _need(rstd, "rstd", like=x, shape=(N, groups), dtype=torch.float32)
+    _need(dy, "dy", like=x, shape=x.shape, contiguous=False)
+    _, _, _, lddy = _images(dy, "dy", like=x, dtype=x.dtype)
+    dx = empty_rows(x.shape, x.dtype, x.device)
+    _, _, _, lddx = _images(dx)
+    mk = (lambda: torch.empty(Cn, dtype=torch.float32, device=x.device))
+    dw, db = (mk(), mk()) if want_wgrad else (None, None)
+    nws = gn_groupnorm_bwd_workspace(N, S, Cn, groups, _dt(x))
+    ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=x.device)
+    check(gn_groupnorm_bwd(_ptr(x), _ptr(w), _ptr(b), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(db),
+                           _ptr(ws), nws, N, S, Cn, groups, ld, lddy, lddx, _epi(epilogue), _dt(x), _stream(stream)),
+          "gn_groupnorm_bwd")
+    return dx, dw, db
+
+
+FP8_BLOCK = 128  # values that share one scale
+
+
+def _blocks(n):
+    return -(-n // FP8_BLOCK)
+
+
+def _codes(rows, cols, device):
+    torch = _torch()
+    return empty_rows((rows, cols), torch.float8_e4m3fn, device)
+
+
+@_placed
+def norm_quant_fp8(x, g=None, beta=None, eps=1e-6, norm="rms", gemma=False, epilogue="none", save_stats=True, stream=None):
+    """epi(norm(x)) of the rows of x [..., hidden] in 8 bits, one scale per 128 values of a row ->
+    (codes [rows, hidden] float8_e4m3fn, scales [rows, ceil(hidden / 128)] fp32, mean, rstd) (statistics
+    fp32 [rows], None where the norm has none)."""
+    torch = _torch()
+    rows, hidden, ld = _rows16(x)
+    kind = _norm(norm)
+    _need(g, "g", like=x, shape=(hidden,), dtype=x.dtype, optional=True)
+    _need(beta, "beta", like=x, shape=(hidden,), dtype=x.dtype, optional=True)
+    q = _codes(rows, hidden, x.device)
+    s = torch.empty((rows, _blocks(hidden)), dtype=torch.float32, device=x.device)
+    mu = torch.empty(rows, dtype=torch.float32, device=x.device) if save_stats and kind == GN_NORM_LN else None
+    rs = torch.empty(rows, dtype=torch.float32, device=x.device) if save_stats and kind != GN_NORM_NONE else None
+    check(gn_norm_quant_fp8(_ptr(x), _ptr(g), _ptr(beta), _ptr(q), _ptr(s), _ptr(mu), _ptr(rs), rows, hidden, ld,
+                            _rows16(q)[2], _ld(s), eps, kind, int(gemma), _epi(epilogue), _dt(x), _stream(stream)),
+          "gn_norm_quant_fp8")
+    return q, s, mu, rs
+
+
+def _ld(t):
+    """row stride of a scale matrix (its width where one row or none leaves the stride open)"""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+@_placed
+def _quant_fp8(x, dy, tile, by_rows, transposed, want_db, epilogue, stream=None):
+    torch = _torch()
+    _need(x, "x", contiguous=False)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    rows, cols, ld = _rows16(x)
+    lddy = 0
+    if dy is not None:
+        _need(dy, "dy", like=x, shape=x.shape, contiguous=False)
+        _, _, lddy = _rows16(dy, "dy", like=x, dtype=x.dtype)
+    mk = (lambda r, c: torch.empty((r, c), dtype=torch.float32, device=x.device))
+    q = _codes(rows, cols, x.device) if by_rows else None
+    s = mk(_blocks(rows) if tile else rows, _blocks(cols)) if by_rows else None
+    qt = _codes(cols, rows, x.device) if transposed else None
+    st = mk(_blocks(cols) if tile else cols, _blocks(rows)) if transposed else None
+    db = torch.empty(cols, dtype=torch.float32, device=x.device) if want_db else None
+    nws = gn_quant_fp8_workspace(rows, cols) if want_db else 0
+    ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=x.device) if want_db else None
+    check(gn_quant_fp8(_ptr(x), _ptr(dy), _ptr(q), _ptr(s), _ptr(qt), _ptr(st), _ptr(db), _ptr(ws), nws, rows, cols, ld,
+                       lddy, 0 if q is None else _rows16(q)[2], 0 if s is None else _ld(s), 0 if qt is None else _rows16(qt)[2],
+                       0 if st is None else _ld(st), GN_FP8_TILE if tile else GN_FP8_VEC, _epi(epilogue), _dt(x),
+                       _stream(stream)), "gn_quant_fp8")
+    return q, s, qt, st, db
+
+
+def quant_fp8(x, tile=False, by_rows=True, transposed=False, stream=None):
+    """x [rows, cols] in 8 bits, by rows and / or transposed, in one pass -> (codes, scales), (codes_t,
+    scales_t) or all four. tile False: one scale per 128 values of a row (of the transpose's rows for
+    codes_t); tile True: one per 128 x 128 block (a weight)."""
+    if not by_rows and not transposed:
+        raise ValueError("by_rows or transposed must be set")
+    q, s, qt, st, _ = _quant_fp8(x, None, tile, by_rows, transposed, False, "none", stream=stream)
+    return (q, s, qt, st) if by_rows and transposed else (q, s) if by_rows else (qt, st)
+
+
+def act_grad_quant_fp8(z, dy, epilogue="silu", want_db=True, stream=None):
+    """dz = dy * act'(z) [tokens, N] as the operands of its layer's gradient products: 8-bit by rows (for
+    dx = dz W) and transposed (for dW = dz^T x), with the bias gradient -> (codes, scales, codes_t,
+    scales_t, db [N] fp32 or None)."""
+    _need(dy, "dy", contiguous=False)
+    return _quant_fp8(z, dy, False, True, True, want_db, epilogue, stream=stream)
+
+
+@_placed
+def linear_fp8(a, sa, b, sb, d=None, epilogue="none", out=None, out_dtype=None, accumulate=False, stream=None):
+    """y [M, N] = act(a b^T + d) of 8-bit a [M, K], b [N, K] (float8_e4m3fn) with block scales sa
+    [M, ceil(K / 128)] and sb [ceil(N / 128), ceil(K / 128)] (128 x 128 blocks) or [N, ceil(K / 128)]. y is
+    bf16, or fp32 (out_dtype float32: no activation; accumulate adds to `out`)."""
+    torch = _torch()
+    _, _, lda = _rows16(a, "a", dtype=torch.float8_e4m3fn)
+    _, _, ldb = _rows16(b, "b", like=a, dtype=torch.float8_e4m3fn)
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} must be [M, K] and [N, K]")
+    (M, K), N = a.shape, b.shape[0]
+    _need(sa, "sa", like=a, shape=(M, _blocks(K)), dtype=torch.float32, contiguous=False)
+    _need(sb, "sb", like=a, dtype=torch.float32, contiguous=False)
+    if tuple(sb.shape) not in ((_blocks(N), _blocks(K)), (N, _blocks(K))):
+        raise ValueError(f"sb has shape {tuple(sb.shape)}, expected {(_blocks(N), _blocks(K))} or {(N, _blocks(K))}")
+    for t, name in ((sa, "sa"), (sb, "sb")):
+        if t.numel() and t.stride(-1) != 1 and t.shape[1] > 1:
+            raise ValueError(f"last dimension of {name} must be contiguous")
+    _need(d, "d", like=a, shape=(N,), dtype=torch.float32, optional=True)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        y = empty_rows((M, N), out_dtype or torch.bfloat16, a.device)
+    else:
+        y = out
+    _need(y, "out", like=a, shape=(M, N), contiguous=False)
+    _, _, ldy = _rows16(y, "out", like=a, dtype=out_dtype or y.dtype)
+    check(gn_linear_fp8(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(d), _ptr(y), M, N, K, lda, _ld(sa), ldb, _ld(sb),
+                        ldy, FP8_BLOCK if sb.shape[0] == _blocks(N) else 1, int(accumulate), _epi(epilogue), _dt(y),
+                        _stream(stream)), "gn_linear_fp8")
+    return y
 
 
 def torch_empty_like(t):
