@@ -268,7 +268,7 @@ def check_product(y, ops, act, out):
 # odd lengths, widths that end inside a tile
 PRODUCTS = [(1, 128, 128), (1, 5120, 5120), (2, 77, 300), (7, 1000, 1), (16, 256, 64), (17, 129, 127), (31, 513, 4093), (64, 640, 1280),
             (100, 8, 256), (128, 128, 384), (129, 257, 129), (200, 1288, 1000), (333, 300, 2049), (513, 770, 640), (1000, 1000, 1000),
-            (2050, 260, 136)]
+            (2050, 260, 136), (2600, 1030, 520), (4100, 900, 129), (6000, 1290, 1)]
 
 
 @pytest.mark.gpu
@@ -318,7 +318,7 @@ def test_linear_strides_and_neighbours(gpu):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,N,K", [(4, 256, 512), (300, 520, 512)])
+@pytest.mark.parametrize("M,N,K", [(4, 256, 512), (300, 520, 512), (3000, 2000, 512)])
 def test_linear_nan_and_infinite_scales(gpu, M, N, K):
     """NaN codes or scales reach their own row (or weight block of columns) and nothing else."""
     aq, sa, bq, sb, d = operands(M, N, K, 128)
@@ -348,7 +348,7 @@ def test_linear_empty(gpu):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,N,K,b_rows", [(1, 5120, 5120, 128), (48, 1000, 4000, 128), (600, 1300, 1500, 128), (700, 900, 3001, 1)])
+@pytest.mark.parametrize("M,N,K,b_rows", [(1, 5120, 5120, 128), (48, 1000, 4000, 128), (600, 1300, 1500, 128), (700, 900, 3001, 1), (3000, 2000, 1500, 128), (3000, 2000, 1601, 1)])
 def test_same_bits_every_run(gpu, M, N, K, b_rows):
     ops = operands(M, N, K, b_rows)
     dt = torch.float32 if b_rows == 1 else torch.bfloat16
@@ -358,7 +358,7 @@ def test_same_bits_every_run(gpu, M, N, K, b_rows):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [3, 500])
+@pytest.mark.parametrize("M", [3, 500, 5000])
 def test_captured_and_replayed_on_new_inputs(gpu, M):
     N, K = 640, 1100
     W = padded(torch.randn(N, K), torch.bfloat16)

@@ -44,6 +44,8 @@ def _deps():
 # the files the row-normalization and RoPE kernels (and their column reduction) are built from;
 # the tensor-core products live in other files
 STEP_SOURCES = ("api.cu", "rmsnorm.cu", "layernorm.cu", "norm_fwd_warp.cu", "rope.cu")
+# headers that none of them includes
+TENSOR_CORE_HEADERS = ("tcgen05.cuh",)
 
 
 def sources_digest(step_only: bool = False) -> str:
@@ -52,8 +54,10 @@ def sources_digest(step_only: bool = False) -> str:
     import hashlib
 
     srcs = [p for p in sources() if not step_only or os.path.basename(p) in STEP_SOURCES]
+    hdrs = [p for p in glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+            if not step_only or os.path.basename(p) not in TENSOR_CORE_HEADERS]
     h = hashlib.sha256()
-    for p in sorted(srcs + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))):
+    for p in sorted(srcs + hdrs):
         h.update(os.path.basename(p).encode())
         h.update(open(p, "rb").read())
     return h.hexdigest()[:16]

@@ -1,81 +1,628 @@
-// linear_fp8.cu - matrix product of two 8-bit (e4m3) operands with block scales:
+// linear_fp8.cu - matrix product of two 8-bit (e4m3) operands with block scales, on the tcgen05
+// tensor cores:
 //   y[m, n] = act( sum_b sa[m, b] sb[n', b] sum_{k in block b} A[m, k] B[n, k]  + d[n] ),
 // b over the blocks of 128 of the contraction, n' = n / 128 (a weight's 128 x 128 blocks) or n.
-// A product of two e4m3 values is exact in fp32; the block sums and the scaled total are fp32.
+//
+// The scales change with b, so the tensor cores may only sum within a block: every block's product is
+// a fresh accumulator in tensor memory, which warps read back and add, scaled, to the running total
+// in their registers (fp32 throughout; a product of two e4m3 values is exact). Two accumulators
+// alternate, so the tensor cores form block b + 1 while block b is added. For a 128 x 256 share per SM a
+// block takes the tensor cores 128 * 256 * 128 / 8192 = 512 cycles; the adding takes 8 warps 256 cycles
+// of tensor-memory reads and 128 of packed FMAs on each scheduler, in the shade of the former.
+//
+// Two kernels, by shape (see fp8_run):
+//   * linear_fp8_pair_kernel: pairs of SMs on 256 x 256 tiles (tcgen05.mma.cta_group::2, M = 256,
+//     N = 256, K = 32), persistent over the tiles: the work that bounds it is the tensor cores'.
+//   * linear_fp8_split_kernel: the operands' roles exchanged (B's rows on the 128 lanes, 16 to 128 rows
+//     of A as columns) and the contraction split over the CTAs of a cluster, whose partial totals meet
+//     in distributed shared memory in a fixed order: for few rows, where reading B bounds it and every SM
+//     has to read, and for outputs of few tiles.
+// Every mbarrier wait is bounded; a timeout records the error bit, and the CTA leaves its loops, waits
+// for its own tensor-core work and copies, frees its tensor memory and exits.
 #include "gn_common.cuh"
 #include "gn_host.h"
+#include "tcgen05.cuh"
 
 namespace gn {
 namespace {
 
+constexpr int kBlk = 128;                // values that share a scale; also the tile depth
+constexpr uint32_t kTileBytes = 128 * kBlk;  // 128 rows of one block: 16 KiB
 constexpr int64_t kMaxRows = 65535ll * 128;
-constexpr int kT = 64, kKC = 32, kBlk = 128;
 
 struct Fp8Args {
-  const uint8_t* A;
   const float* sa;
-  const uint8_t* B;
   const float* sb;
-  const float* d;
-  void* y;
-  int64_t M, N, K, lda, ldsa, ldb, ldsb, ldy;
-  int b_rows, accumulate;
+  const float* d;  // [N] or null
+  void* y;         // split kernel (the pair kernel writes through its tensor map)
+  int M, N, K, nkb;
+  int64_t ldsa, ldsb, ldy;
+  int accumulate;
+  int b_shift;     // 7: sb has a row per 128 rows of B; 0: one per row
+  unsigned* err;
 };
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  float f;
-  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"((uint16_t)(h & 0xffff)));
-  return f;
+// instruction descriptor of tcgen05.mma kind::f8f6f4: D fp32 (bits 4-5 = 1), A and B e4m3 (0), both
+// K-major, N >> 3 at bit 17, M >> 4 at bit 24
+constexpr uint32_t idesc_f8(int m, int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24); }
+
+// K-major tile of 128-byte rows, 128-byte swizzle (the layout TMA writes): see norm_linear.cu. One
+// instruction's 32 values of the contraction are 32 bytes, two descriptor units.
+__device__ __forceinline__ uint64_t f8_desc(const void* tile) {
+  return (uint64_t)((smem_addr(tile) & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
 }
 
-template <int EPI, bool F32>
-__global__ void __launch_bounds__(256) linear_fp8_simple_kernel(const Fp8Args a) {
-  __shared__ float As[kKC][kT + 1], Bs[kKC][kT + 1];
-  const int64_t m0 = (int64_t)blockIdx.y * kT, n0 = (int64_t)blockIdx.x * kT;
-  const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-  float acc[4][4] = {}, part[4][4] = {};
-  for (int64_t k0 = 0; k0 < a.K; k0 += kKC) {
-    for (int i = threadIdx.x; i < kT * kKC; i += 256) {
-      const int r = i / kKC, k = i % kKC;
-      const bool kin = k0 + k < a.K;
-      As[k][r] = kin && m0 + r < a.M ? e4m3_to_f32(a.A[(m0 + r) * a.lda + k0 + k]) : 0.0f;
-      Bs[k][r] = kin && n0 + r < a.N ? e4m3_to_f32(a.B[(n0 + r) * a.ldb + k0 + k]) : 0.0f;
+template <int CG, int M, int N>
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc_f8(M, N)), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc_f8(M, N)), "r"(accumulate)
+        : "memory");
+}
+
+// 16 consecutive columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2 (&v)[8]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+
+// arrive on the barrier at this shared::cluster address (either CTA's), releasing at cluster scope
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// mbar_wait whose success also acquires what the other CTA of the pair released
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, unsigned* err) {
+  const bool ok = mbar_wait(bar, parity, err);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return ok;
+}
+
+// the activation of bf16 outputs: the hardware tanh, the approximate exponential and divide
+template <int EPI>
+__device__ __forceinline__ float f8_act(float z) {
+  if constexpr (EPI == EPI_SILU)
+    return __fdividef(z, 1.0f + __expf(-z));
+  else
+    return epi_fwd<EPI, true>(z);
+}
+
+// ---------------------------------------------------------------- pairs of SMs
+// Warp 0 loads (each CTA its 128 rows of A and its half of B's 256 rows per stage), warp 1 of the leader
+// issues the instructions, warps 4-11 of each CTA own 128 rows x 256 columns of totals: warp w the rows
+// 32 (w % 4).. (the tensor-memory lanes it may read) and the column half w / 4 - 1, one row and 128
+// columns a thread. The 128 totals a thread do not fit the 168 registers of an even split: the first four
+// warps give theirs up (3 x 168 = 72 + 2 x 216 a thread and scheduler).
+constexpr int kPairThreads = 384;
+constexpr uint32_t kPairStage = 2 * kTileBytes;
+constexpr uint32_t kBoxBytes = 32 * 128;  // one output box of a warp: 32 rows x 128 bytes
+template <bool BROW>
+struct Pair {
+  static constexpr int Stages = BROW ? 5 : 6;
+  static constexpr size_t Smem = 1024 + (size_t)Stages * kPairStage + 8 * kBoxBytes + 256 + (BROW ? 2 * 256 * 4 : 0);
+};
+
+template <int EPI, bool F32, bool BROW>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmY, const Fp8Args a) {
+  constexpr int kStages = Pair<BROW>::Stages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* boxes = smem + kStages * kPairStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 8 * kBoxBytes);  // leader: both CTAs' tiles landed
+  uint64_t* empty = full + kStages;   // the pair's instructions are done with the stage
+  uint64_t* accf = empty + kStages;   // [2] accumulator formed
+  uint64_t* acce = accf + 2;          // [2] leader: accumulator read by all 16 warps
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(acce + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  float* sb_row = reinterpret_cast<float*>(boxes + 8 * kBoxBytes + 256);  // BROW: [2][256]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int nt = (a.N + 255) / 256, mt = (a.M + 255) / 256;
+  const int64_t tiles = (int64_t)nt * mt;
+  const int64_t step = gridDim.x >> 1;
+  auto A = [&](int s) { return smem + s * kPairStage; };
+  auto B = [&](int s) { return smem + s * kPairStage + kTileBytes; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
-    __syncthreads();
-    for (int k = 0; k < kKC; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) part[i][j] = fmaf(As[k][tr * 4 + i], Bs[k][tc * 4 + j], part[i][j]);
-    __syncthreads();
-    if ((k0 + kKC) % kBlk == 0 || k0 + kKC >= a.K) {
-      const int64_t b = k0 / kBlk;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t m = m0 + tr * 4 + i, n = n0 + tc * 4 + j;
-          if (m < a.M && n < a.N) acc[i][j] = fmaf(a.sa[m * a.ldsa + b] * a.sb[n / a.b_rows * a.ldsb + b], part[i][j], acc[i][j]);
-          part[i][j] = 0.0f;
-        }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&accf[i], 1);
+      mbar_init(&acce[i], 16);
     }
+    *abort_flag = 0;
+    mbar_fence_init();
   }
+  if (warp == 1) tmem_alloc_pair(tslot, 512);
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers exist before any load counts on them
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      uint32_t lastph = 0, used = 0, ph = 0;
+      int s = 0;
+      bool go = true, wrapped = false;
+      for (int64_t t = blockIdx.x >> 1; go && t < tiles; t += step) {
+        const int m0 = (int)(t / nt) * 256 + 128 * (int)rank, n0 = (int)(t % nt) * 256 + 128 * (int)rank;
+        for (int kb = 0; kb < a.nkb; ++kb) {
+          if ((wrapped && !mbar_wait(&empty[s], ph ^ 1u, a.err)) || *abort_flag) {
+            *abort_flag = 1;
+            go = false;
+            break;
+          }
+          const uint32_t bar = cluster_addr(&full[s], 0);
+          if (leader) mbar_expect_tx(&full[s], 2 * kPairStage);  // both CTAs' bytes
+          tma_load_2d_pair(A(s), &tmA, kb * kBlk, m0, bar);
+          tma_load_2d_pair(B(s), &tmB, kb * kBlk, n0, bar);
+          used |= 1u << s;
+          lastph = (lastph & ~(1u << s)) | (ph << s);
+          if (++s == kStages) s = 0, ph ^= 1u, wrapped = true;
+        }
+      }
+      // the leader's barriers count both CTAs' copies: every copy issued has landed once they
+      // complete (bounded waits)
+      if (leader)
+        for (int i = 0; i < kStages; ++i)
+          if (used & (1u << i)) (void)mbar_wait(&full[i], (lastph >> i) & 1u, a.err);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (leader && lane == 0) {
+      uint32_t ph = 0, aph = 0;
+      int s = 0, buf = 0;
+      bool go = true, second = false;  // second: both accumulators have been used once
+      for (int64_t t = blockIdx.x >> 1; go && t < tiles; t += step) {
+        for (int kb = 0; kb < a.nkb; ++kb) {
+          if ((second && !mbar_wait_cluster(&acce[buf], aph ^ 1u, a.err)) || !mbar_wait(&full[s], ph, a.err) ||
+              *abort_flag) {
+            *abort_flag = 1;
+            go = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = f8_desc(A(s)), bd = f8_desc(B(s));
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + tr * 4 + i, n = n0 + tc * 4 + j;
-      if (m >= a.M || n >= a.N) continue;
-      const float z = epi_fwd<EPI, !F32>(acc[i][j] + (a.d ? a.d[n] : 0.0f));
-      if constexpr (F32) {
-        float* p = static_cast<float*>(a.y) + m * a.ldy + n;
-        *p = a.accumulate ? *p + z : z;
-      } else {
-        static_cast<__nv_bfloat16*>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(z);
+          for (int k = 0; k < kBlk / 32; ++k) umma_f8<2, 256, 256>(tmem + 256u * buf, ad + 2 * k, bd + 2 * k, k != 0);
+          umma_commit_pair(&empty[s]);
+          umma_commit_pair(&accf[buf]);
+          if (++s == kStages) s = 0, ph ^= 1u;
+          if (++buf == 2) buf = 0, aph ^= 1u, second = true;
+        }
+      }
+      if (!go) {  // both CTAs' other warps wait for the work in flight
+        umma_commit_pair(&accf[0]);
+        umma_commit_pair(&accf[1]);
       }
     }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ totals and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int q = warp & 3;                // tensor-memory lane quadrant
+    const int half = (warp >> 2) - 1;      // column half
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const uint32_t empty_bar[2] = {cluster_addr(&acce[0], 0), cluster_addr(&acce[1], 0)};
+    uint8_t* box = boxes + (size_t)(warp - 4) * kBoxBytes;
+    const int ct = threadIdx.x - 128;      // 0..255
+    uint32_t ph = 0;
+    int buf = 0, sbuf = 0;
+    bool ok = true, box_used = false;
+    for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += step) {
+      const int m0 = (int)(t / nt) * 256 + 128 * (int)rank, n0 = (int)(t % nt) * 256;
+      const int m = m0 + 32 * q + lane;
+      const int nh = n0 + 128 * half;      // first column of this thread
+      const float* sa = a.sa + (int64_t)(m < a.M ? m : a.M - 1) * a.ldsa;
+      const int nb = nh < a.N ? nh >> 7 : 0;
+      const float* sb = BROW ? a.sb + (int64_t)(n0 + ct < a.N ? n0 + ct : a.N - 1) * a.ldsb : a.sb + (int64_t)nb * a.ldsb;
+      float2 acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
+      float sa_next = __ldg(sa), sb_next = __ldg(sb);
+      for (int kb = 0; kb < a.nkb; ++kb) {
+        const float sav = sa_next, sbv = sb_next;
+        if constexpr (BROW) {
+          sb_row[sbuf * 256 + ct] = sbv;  // this half's readers have passed the last barrier
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
+        if (kb + 1 < a.nkb) sa_next = __ldg(sa + kb + 1), sb_next = __ldg(sb + kb + 1);
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&accf[buf], ph, a.err)) && !*abort_flag;
+        if (!ok && !BROW) break;  // BROW: every warp keeps meeting the barrier, to the end of the tile
+        tc_fence_after();
+        if (ok) {
+          const float2 f = dup2(BROW ? sav : sav * sbv);
+          const float* sr = sb_row + sbuf * 256 + 128 * half;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float2 p[8];
+            tmem_ld16(tmem + lanes + 256u * buf + 128u * half + 16u * c, p);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              if constexpr (BROW) {
+                const float4 s4 = *reinterpret_cast<const float4*>(sr + 16 * c + 2 * i);
+                acc[8 * c + i] = fma2(p[i], mul2(f, make_float2(s4.x, s4.y)), acc[8 * c + i]);
+                acc[8 * c + i + 1] = fma2(p[i + 1], mul2(f, make_float2(s4.z, s4.w)), acc[8 * c + i + 1]);
+              } else {
+                acc[8 * c + i] = fma2(p[i], f, acc[8 * c + i]);
+                acc[8 * c + i + 1] = fma2(p[i + 1], f, acc[8 * c + i + 1]);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(empty_bar[buf]);
+        if (++buf == 2) buf = 0, ph ^= 1u;
+        sbuf ^= 1;
+      }
+      if (!ok) break;
+      // bias, activation, and the way out: boxes of 128 bytes x 32 rows in shared memory (128-byte
+      // swizzle: 16-byte chunk c of row r at position c ^ (r % 8)), written by TMA with the rows and
+      // columns past M and N clipped
+      constexpr int kCols = F32 ? 32 : 64;  // columns of a box
+#pragma unroll
+      for (int b = 0; b < 128 / kCols; ++b) {
+        const int col0 = nh + b * kCols;
+        if (col0 < a.N) {  // uniform over the warp
+          if (box_used) {  // the box's previous store has finished reading it
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+          }
+          uint8_t* row = box + lane * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            constexpr int kE = kCols / 8;  // elements of a 16-byte chunk
+            float o[kE];
+#pragma unroll
+            for (int e = 0; e < kE; e += 2) {
+              const float2 v = acc[(b * kCols + c * kE + e) / 2];
+              const int n = col0 + c * kE + e;
+              o[e] = v.x + (a.d && n < a.N ? __ldg(a.d + n) : 0.0f);
+              o[e + 1] = v.y + (a.d && n + 1 < a.N ? __ldg(a.d + n + 1) : 0.0f);
+              if constexpr (!F32) o[e] = f8_act<EPI>(o[e]), o[e + 1] = f8_act<EPI>(o[e + 1]);
+            }
+            uint4 w;
+            if constexpr (F32) w = Vec<float>::pack(o);
+            else w = Vec<__nv_bfloat16>::pack(o);
+            *reinterpret_cast<uint4*>(row + ((c ^ (lane & 7)) << 4)) = w;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (F32 && a.accumulate) tma_reduce_add_2d(&tmY, box, col0, m0 + 32 * q);
+            else tma_store_2d(&tmY, box, col0, m0 + 32 * q);
+          }
+          box_used = true;
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_read<0>();  // the boxes are read before the CTA may leave
+    __syncwarp();
+  }
+
+  // teardown: neither CTA leaves while the pair's instructions may still touch its shared or tensor
+  // memory; then both free the pair's tensor memory
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- few rows: roles exchanged, split contraction
+// A cluster of CS CTAs shares one output tile of 128 columns n x MT rows m; its CTA r sums the blocks
+// [r nkb / CS, (r + 1) nkb / CS) with B's 128 rows on the tensor-memory lanes (one n a thread) and MT
+// columns m. The totals go to shared memory, [m][n] fp32; after a cluster barrier CTA r adds the CS
+// copies of its share of the rows m in rank order and writes it.
+constexpr int kSplitThreads = 192;
+template <int MT>
+struct Split {
+  static constexpr uint32_t Stage = kTileBytes + MT * kBlk;
+  static constexpr int Stages = MT == 16 ? 6 : MT == 32 ? 5 : MT == 64 ? 4 : 3;  // two CTAs per SM
+  static constexpr uint32_t TmemCols = 2 * MT;
+  static constexpr size_t Smem = 1024 + (size_t)Stages * Stage + 256 + 2 * MT * 4;
+  static_assert((size_t)Stages * Stage >= (size_t)MT * 128 * 4, "the totals reuse the stages");
+};
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int MT, int EPI, bool F32>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+    linear_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                            const Fp8Args a, int cs) {
+  using SP = Split<MT>;
+  constexpr int kStages = SP::Stages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * SP::Stage);
+  uint64_t* empty = full + kStages;
+  uint64_t* accf = empty + kStages;  // [2]
+  uint64_t* acce = accf + 2;         // [2]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(acce + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  float* sa_col = reinterpret_cast<float*>(smem + kStages * SP::Stage + 256);  // [2][MT]
+  float* total = reinterpret_cast<float*>(smem);                              // [MT][128]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int n0 = (int)(blockIdx.x / cs) * 128, m0 = (int)blockIdx.y * MT;
+  const int kb0 = (int)((int64_t)rank * a.nkb / cs), kb1 = (int)((int64_t)(rank + 1) * a.nkb / cs);
+  auto W = [&](int s) { return smem + s * SP::Stage; };
+  auto X = [&](int s) { return smem + s * SP::Stage + kTileBytes; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&accf[i], 1);
+      mbar_init(&acce[i], 4);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc(tslot, SP::TmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  bool ok = true;
+  float acc[MT];
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t lastph = 0, used = 0, ph = 0;
+      int s = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if ((kb - kb0 >= kStages && !mbar_wait(&empty[s], ph ^ 1u, a.err)) || *abort_flag) {
+          *abort_flag = 1;
+          break;
+        }
+        mbar_expect_tx(&full[s], SP::Stage);
+        tma_load_2d(W(s), &tmB, kb * kBlk, n0, &full[s]);
+        tma_load_2d(X(s), &tmA, kb * kBlk, m0, &full[s]);
+        used |= 1u << s;
+        lastph = (lastph & ~(1u << s)) | (ph << s);
+        if (++s == kStages) s = 0, ph ^= 1u;
+      }
+      for (int i = 0; i < kStages; ++i)
+        if (used & (1u << i)) (void)mbar_wait(&full[i], (lastph >> i) & 1u, a.err);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t ph = 0;
+      int s = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int i = kb - kb0, buf = i & 1;
+        if ((i >= 2 && !mbar_wait(&acce[buf], (uint32_t)((i >> 1) - 1) & 1u, a.err)) || !mbar_wait(&full[s], ph, a.err) ||
+            *abort_flag) {
+          *abort_flag = 1;
+          umma_commit(&accf[0]);
+          umma_commit(&accf[1]);
+          break;
+        }
+        tc_fence_after();
+        const uint64_t wd = f8_desc(W(s)), xd = f8_desc(X(s));
+#pragma unroll
+        for (int k = 0; k < kBlk / 32; ++k) umma_f8<1, 128, MT>(tmem + (uint32_t)(MT * buf), wd + 2 * k, xd + 2 * k, k != 0);
+        umma_commit(&empty[s]);
+        umma_commit(&accf[buf]);
+        if (++s == kStages) s = 0, ph ^= 1u;
+      }
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    const int ct = threadIdx.x - 64;   // 0..127
+    const int n = n0 + 32 * q + lane;  // this thread's column of y
+    const float* sb = a.sb + (int64_t)((n < a.N ? n : a.N - 1) >> a.b_shift) * a.ldsb;
+    const float* sa = a.sa + (int64_t)(m0 + ct < a.M ? m0 + ct : a.M - 1) * a.ldsa;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = 0.0f;
+    float sb_next = kb0 < kb1 ? __ldg(sb + kb0) : 0.0f, sa_next = kb0 < kb1 && ct < MT ? __ldg(sa + kb0) : 0.0f;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int i = kb - kb0, buf = i & 1;
+      const float sbv = sb_next;
+      if (ct < MT) sa_col[buf * MT + ct] = sa_next;  // last read before the barrier of the block before
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (kb + 1 < kb1) {
+        sb_next = __ldg(sb + kb + 1);
+        if (ct < MT) sa_next = __ldg(sa + kb + 1);
+      }
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&accf[buf], (uint32_t)(i >> 1) & 1u, a.err)) && !*abort_flag;
+      tc_fence_after();
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < MT / 16; ++c) {
+          float2 p[8];
+          tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(MT * buf + 16 * c), p);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float4 s4 = *reinterpret_cast<const float4*>(sa_col + buf * MT + 16 * c + 2 * e);
+            float* t = acc + 16 * c + 2 * e;
+            t[0] = fmaf(p[e].x, sbv * s4.x, t[0]);
+            t[1] = fmaf(p[e].y, sbv * s4.y, t[1]);
+            t[2] = fmaf(p[e + 1].x, sbv * s4.z, t[2]);
+            t[3] = fmaf(p[e + 1].y, sbv * s4.w, t[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&acce[buf]);
+    }
+  }
+  // the stages are free once the last accumulator is formed (its blocks' tiles have been read); every
+  // warp meets here, then the totals take their place
+  __syncthreads();
+  if (warp >= 2) {
+    const int nl = 32 * (warp & 3) + lane;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) total[i * 128 + nl] = acc[i];
+  }
+  if (cs > 1) cluster_sync_all();
+  else __syncthreads();
+  if (!*abort_flag && warp >= 2) {
+    const int nl = threadIdx.x - 64, n = n0 + nl;
+    const float d = a.d && n < a.N ? a.d[n] : 0.0f;
+    const int i0 = MT * rank / cs, i1 = MT * (rank + 1) / cs;
+    uint32_t peer[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) peer[j] = cluster_addr(total, j < cs ? (uint32_t)j : 0u);
+    for (int i = i0; i < i1; ++i) {
+      const int m = m0 + i;
+      if (m >= a.M) break;
+      float z = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < cs) z += ld_cluster(peer[j] + (uint32_t)(i * 128 + nl) * 4u);
+      z += d;
+      if (n < a.N) {
+        if constexpr (F32) {
+          float* p = static_cast<float*>(a.y) + (int64_t)m * a.ldy + n;
+          *p = a.accumulate ? *p + z : z;
+        } else {
+          static_cast<__nv_bfloat16*>(a.y)[(int64_t)m * a.ldy + n] = __float2bfloat16_rn(f8_act<EPI>(z));
+        }
+      }
+    }
+  }
+  // no CTA leaves while another may read its totals
+  if (cs > 1) cluster_sync_all();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, SP::TmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+// codes [rows, K] with row stride ld, boxes of box_rows x 128 values, 128-byte swizzle; outside: zeros
+bool make_code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld, uint32_t box_rows) {
+  EncodeTiled enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t box[2] = {kBlk, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// y [rows, cols]: boxes of 32 rows x 128 bytes
+bool make_y_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld, bool f32) {
+  EncodeTiled enc = encode_fn();
+  if (!enc) return false;
+  const size_t es = f32 ? 4 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(ld * es)};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32u};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BROW>
+void* pick_pair(int epi, bool f32) {
+  return f32                       ? (void*)linear_fp8_pair_kernel<EPI_NONE, true, BROW>
+         : epi == GN_EPI_GELU_TANH ? (void*)linear_fp8_pair_kernel<EPI_GELU_TANH, false, BROW>
+         : epi == GN_EPI_SILU      ? (void*)linear_fp8_pair_kernel<EPI_SILU, false, BROW>
+                                   : (void*)linear_fp8_pair_kernel<EPI_NONE, false, BROW>;
+}
+
+template <int MT>
+void* pick_split(int epi, bool f32) {
+  return f32                       ? (void*)linear_fp8_split_kernel<MT, EPI_NONE, true>
+         : epi == GN_EPI_GELU_TANH ? (void*)linear_fp8_split_kernel<MT, EPI_GELU_TANH, false>
+         : epi == GN_EPI_SILU      ? (void*)linear_fp8_split_kernel<MT, EPI_SILU, false>
+                                   : (void*)linear_fp8_split_kernel<MT, EPI_NONE, false>;
+}
+
+gn_status fp8_run(const void* A, int64_t lda, const void* B, int64_t ldb, Fp8Args a, int epi, bool f32,
+                  cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return GN_ERR_CUDA;
+  const int64_t pairs = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+  CUtensorMap ta, tb, ty;
+  if (a.N > 128 && a.M > 128 && pairs >= sms / 4) {
+    if (!make_code_map(&ta, A, a.M, a.K, lda, 128) || !make_code_map(&tb, B, a.N, a.K, ldb, 128) ||
+        !make_y_map(&ty, a.y, a.M, a.N, a.ldy, f32))
+      return GN_ERR_CUDA;
+    const bool brow = a.b_shift == 0;
+    void* kern = brow ? pick_pair<true>(epi, f32) : pick_pair<false>(epi, f32);
+    const size_t smem = brow ? Pair<true>::Smem : Pair<false>::Smem;
+    if (!kernel_attrs(kern, smem)) return GN_ERR_CUDA;
+    const int64_t clusters = pairs < sms / 2 ? pairs : sms / 2;
+    void* args[] = {&ta, &tb, &ty, &a};
+    if (cudaLaunchKernel(kern, dim3((unsigned)(2 * clusters)), dim3(kPairThreads), args, smem, stream) != cudaSuccess)
+      return GN_ERR_CUDA;
+    count_launches(1);
+    return launch_status();
+  }
+  const int MT = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+  const int64_t tiles = (int64_t)((a.N + 127) / 128) * ((a.M + MT - 1) / MT);
+  int cs = 1;
+  while (cs < 8 && tiles * cs < 2 * sms && a.nkb >= 4 * cs) cs *= 2;
+  if (!make_code_map(&ta, A, a.M, a.K, lda, (uint32_t)MT) || !make_code_map(&tb, B, a.N, a.K, ldb, 128)) return GN_ERR_CUDA;
+  void* kern = MT == 16   ? pick_split<16>(epi, f32)
+               : MT == 32 ? pick_split<32>(epi, f32)
+               : MT == 64 ? pick_split<64>(epi, f32)
+                          : pick_split<128>(epi, f32);
+  const size_t smem = MT == 16 ? Split<16>::Smem : MT == 32 ? Split<32>::Smem : MT == 64 ? Split<64>::Smem : Split<128>::Smem;
+  if (!kernel_attrs(kern, smem)) return GN_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(cs * ((a.N + 127) / 128)), (unsigned)((a.M + MT - 1) / MT));
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {&ta, &tb, &a, &cs};
+  if (cudaLaunchKernelExC(&cfg, kern, args) != cudaSuccess) return GN_ERR_CUDA;
+  count_launches(1);
+  return launch_status();
 }
 
 }  // namespace
@@ -88,27 +635,23 @@ extern "C" gn_status gn_linear_fp8(const void* A, const float* sa, const void* B
                                    int64_t ld_sb, int64_t ld_y, int64_t b_rows, int accumulate, gn_epilogue epi,
                                    gn_dtype out, void* stream) {
   if (!dt_ok(out) || !epi_ok(epi)) return GN_ERR_DTYPE;
-  const int64_t kb = (K + kBlk - 1) / kBlk;
-  if (M < 0 || N < 0 || K <= 0 || M > kMaxRows || N > INT32_MAX || K > INT32_MAX || (b_rows != 1 && b_rows != kBlk))
+  if (M < 0 || N < 0 || K <= 0 || M > kMaxRows || N > kMaxRows || K > INT32_MAX - kBlk || (b_rows != 1 && b_rows != kBlk))
     return GN_ERR_SHAPE;
+  const int64_t kb = (K + kBlk - 1) / kBlk;
   if (ld_a < K || ld_b < K || ld_sa < kb || ld_sb < kb || ld_y < N) return GN_ERR_SHAPE;
   if (out == GN_F32 ? epi != GN_EPI_NONE : accumulate != 0) return GN_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return GN_OK;
   if (!A || !sa || !B || !sb || !y) return GN_ERR_NULL;
   if (!aligned16(A) || !aligned16(B) || !aligned16(y) || ld_a % 16 || ld_b % 16 || ld_y * dt_size(out) % 16 ||
-      (d && !aligned16(d)) || (reinterpret_cast<uintptr_t>(sa) & 3) ||
-      (reinterpret_cast<uintptr_t>(sb) & 3))
+      (d && !aligned16(d)) || (reinterpret_cast<uintptr_t>(sa) & 3) || (reinterpret_cast<uintptr_t>(sb) & 3))
     return GN_ERR_ALIGN;
-  Fp8Args a{static_cast<const uint8_t*>(A), sa, static_cast<const uint8_t*>(B), sb, d, y, M, N, K, ld_a, ld_sa, ld_b, ld_sb,
-            ld_y, (int)b_rows, accumulate != 0};
-  void* kern = out == GN_F32             ? (void*)linear_fp8_simple_kernel<EPI_NONE, true>
-               : epi == GN_EPI_GELU_TANH ? (void*)linear_fp8_simple_kernel<EPI_GELU_TANH, false>
-               : epi == GN_EPI_SILU      ? (void*)linear_fp8_simple_kernel<EPI_SILU, false>
-                                         : (void*)linear_fp8_simple_kernel<EPI_NONE, false>;
-  const dim3 grid((unsigned)((N + kT - 1) / kT), (unsigned)((M + kT - 1) / kT));
-  if (grid.y > 65535) return GN_ERR_UNSUPPORTED;
-  void* args[] = {&a};
-  if (cudaLaunchKernel(kern, grid, dim3(256), args, 0, (cudaStream_t)stream) != cudaSuccess) return GN_ERR_CUDA;
-  count_launches(1);
-  return launch_status();
+  Fp8Args a{};
+  a.sa = sa, a.sb = sb, a.d = d, a.y = y;
+  a.M = (int)M, a.N = (int)N, a.K = (int)K, a.nkb = (int)kb;
+  a.ldsa = ld_sa, a.ldsb = ld_sb, a.ldy = ld_y;
+  a.accumulate = accumulate != 0;
+  a.b_shift = b_rows == kBlk ? 7 : 0;
+  a.err = device_err_word();
+  if (!a.err) return GN_ERR_CUDA;
+  return fp8_run(A, ld_a, B, ld_b, a, epi, out == GN_F32, (cudaStream_t)stream);
 }
