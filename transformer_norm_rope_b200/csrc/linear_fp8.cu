@@ -86,16 +86,57 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2 (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 
-// arrive on the barrier at this shared::cluster address (either CTA's), releasing at cluster scope
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+// the same for 32 columns, in two steps: the load is issued, and its registers may be used after the wait
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// (the registers pass through the wait so that no use of them can be scheduled before it)
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32], uint32_t (&t)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31]), "+r"(t[0]), "+r"(t[1]), "+r"(t[2]), "+r"(t[3]), "+r"(t[4]),
+                 "+r"(t[5]), "+r"(t[6]), "+r"(t[7]), "+r"(t[8]), "+r"(t[9]), "+r"(t[10]), "+r"(t[11]), "+r"(t[12]),
+                 "+r"(t[13]), "+r"(t[14]), "+r"(t[15]), "+r"(t[16]), "+r"(t[17]), "+r"(t[18]), "+r"(t[19]),
+                 "+r"(t[20]), "+r"(t[21]), "+r"(t[22]), "+r"(t[23]), "+r"(t[24]), "+r"(t[25]), "+r"(t[26]),
+                 "+r"(t[27]), "+r"(t[28]), "+r"(t[29]), "+r"(t[30]), "+r"(t[31])
+               :
+               : "memory");
 }
 
-// mbar_wait whose success also acquires what the other CTA of the pair released
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, unsigned* err) {
-  const bool ok = mbar_wait(bar, parity, err);
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return ok;
+// 32 columns of 16 lanes as fragments: r[4 j + 2 h + e] = (lane of the address) + lane / 4 + 8 h, column
+// 8 j + 2 (lane % 4) + e
+__device__ __forceinline__ void tmem_ld16x32_issue(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// arrive on the barrier at this shared::cluster address (either CTA's). What it orders are tensor-memory
+// reads, by the tcgen05 fences around it; a fence or an arrival that releases ordinary memory to the whole
+// cluster cost more than a block's product (measured at 32768 x 5120 x 5120: 2.5 ms with, see below without).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 // the activation of bf16 outputs: the hardware tanh, the approximate exponential and divide
@@ -112,21 +153,42 @@ __device__ __forceinline__ float f8_act(float z) {
 // issues the instructions, warps 4-11 of each CTA own 128 rows x 256 columns of totals: warp w the rows
 // 32 (w % 4).. (the tensor-memory lanes it may read) and the column half w / 4 - 1, one row and 128
 // columns a thread. The 128 totals a thread do not fit the 168 registers of an even split: the first four
-// warps give theirs up (3 x 168 = 72 + 2 x 216 a thread and scheduler).
+// warps give theirs up (3 x 168 = 40 + 2 x 232 a thread and scheduler).
 constexpr int kPairThreads = 384;
 constexpr uint32_t kPairStage = 2 * kTileBytes;
 constexpr uint32_t kBoxBytes = 32 * 128;  // one output box of a warp: 32 rows x 128 bytes
+// Scales travel in groups of four blocks: warp 3 of each CTA copies, asynchronously and up to kSlots groups
+// ahead, the 128 rows' [row][4] of sa and the tile's [2][4] (or, BROW, [256][4]) of sb. Read row by row where
+// they lie, a block at a time, they cost a quarter more L2 traffic (a 32-byte sector per row and block) and
+// their latency (5120 x 5120 x 4096 with row scales: see the figures below).
+constexpr int kPairStages = 5, kSlots = 4;
 template <bool BROW>
 struct Pair {
-  static constexpr int Stages = BROW ? 5 : 6;
-  static constexpr size_t Smem = 1024 + (size_t)Stages * kPairStage + 8 * kBoxBytes + 256 + (BROW ? 2 * 256 * 4 : 0);
+  static constexpr int SbRows = BROW ? 256 : 2;
+  static constexpr uint32_t Slot = (128 + SbRows) * 16;
+  static constexpr size_t Smem = 1024 + (size_t)kPairStages * kPairStage + 8 * kBoxBytes + 256 + kSlots * Slot;
 };
+
+// one row's scales of blocks b .. b + 3 into 16 bytes of shared memory; blocks at and past nkb, and rows that
+// are not `in`, are zero
+__device__ __forceinline__ void copy_scales(float* dst, const float* row, int b, int nkb, bool in, bool vec) {
+  const int n = !in ? 0 : nkb - b < 4 ? nkb - b : 4;
+  if (vec) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(row + b), "r"(4 * n) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst + i)), "l"(row + (i < n ? b + i : b)),
+                   "r"(i < n ? 4 : 0)
+                   : "memory");
+  }
+}
 
 template <int EPI, bool F32, bool BROW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                            const __grid_constant__ CUtensorMap tmY, const Fp8Args a) {
-  constexpr int kStages = Pair<BROW>::Stages;
+  constexpr int kStages = kPairStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* boxes = smem + kStages * kPairStage;
@@ -134,9 +196,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint64_t* empty = full + kStages;   // the pair's instructions are done with the stage
   uint64_t* accf = empty + kStages;   // [2] accumulator formed
   uint64_t* acce = accf + 2;          // [2] leader: accumulator read by all 16 warps
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(acce + 2);
+  uint64_t* scf = acce + 2;           // [kSlots] a group of scales has landed
+  uint64_t* sce = scf + kSlots;       // [kSlots] it has been read by this CTA's 8 warps
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sce + kSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-  float* sb_row = reinterpret_cast<float*>(boxes + 8 * kBoxBytes + 256);  // BROW: [2][256]
+  float* scales = reinterpret_cast<float*>(boxes + 8 * kBoxBytes + 256);
+  constexpr int kSlotFloats = Pair<BROW>::Slot / 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
@@ -155,6 +220,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(&accf[i], 1);
       mbar_init(&acce[i], 16);
     }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&scf[i], 32);
+      mbar_init(&sce[i], 8);
+    }
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -163,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();  // both CTAs' barriers exist before any load counts on them
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
@@ -194,94 +263,162 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int i = 0; i < kStages; ++i)
           if (used & (1u << i)) (void)mbar_wait(&full[i], (lastph >> i) & 1u, a.err);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (leader)
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------ MMA issuers (leader)
+    // Two warps, each with one of the two accumulators and every other block: the waits of one pass
+    // while the other's instructions run. (A wait on a barrier that is ready costs the issuer about
+    // 180 cycles next to the operand traffic in shared memory; one issuer's two waits a block left
+    // the tensor cores idle that long.)
     if (leader && lane == 0) {
-      uint32_t ph = 0, aph = 0;
-      int s = 0, buf = 0;
-      bool go = true, second = false;  // second: both accumulators have been used once
-      for (int64_t t = blockIdx.x >> 1; go && t < tiles; t += step) {
-        for (int kb = 0; kb < a.nkb; ++kb) {
-          if ((second && !mbar_wait_cluster(&acce[buf], aph ^ 1u, a.err)) || !mbar_wait(&full[s], ph, a.err) ||
-              *abort_flag) {
-            *abort_flag = 1;
-            go = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ad = f8_desc(A(s)), bd = f8_desc(B(s));
-#pragma unroll
-          for (int k = 0; k < kBlk / 32; ++k) umma_f8<2, 256, 256>(tmem + 256u * buf, ad + 2 * k, bd + 2 * k, k != 0);
-          umma_commit_pair(&empty[s]);
-          umma_commit_pair(&accf[buf]);
-          if (++s == kStages) s = 0, ph ^= 1u;
-          if (++buf == 2) buf = 0, aph ^= 1u, second = true;
+      const int buf = warp - 1;
+      const int64_t mine = blockIdx.x >> 1 < tiles ? (tiles - 1 - (blockIdx.x >> 1)) / step + 1 : 0;
+      const int64_t blocks = mine * a.nkb;
+      uint32_t full_ph = 0, acc_ph = 1;
+      int s = buf;
+      bool go = true;
+      for (int64_t i = buf; i < blocks; i += 2) {
+        if ((i >= 2 && !mbar_wait(&acce[buf], acc_ph, a.err)) || !mbar_wait(&full[s], full_ph, a.err)) {
+          go = false;
+          break;
         }
+        tc_fence_after();
+        const uint64_t ad = f8_desc(A(s)), bd = f8_desc(B(s));
+#pragma unroll
+        for (int k = 0; k < kBlk / 32; ++k) umma_f8<2, 256, 256>(tmem + 256u * buf, ad + 2 * k, bd + 2 * k, k != 0);
+        umma_commit_pair(&accf[buf]);
+        umma_commit_pair(&empty[s]);
+        acc_ph ^= 1u;
+        s += 2;
+        if (s >= kStages) s -= kStages, full_ph ^= 1u;
       }
       if (!go) {  // both CTAs' other warps wait for the work in flight
-        umma_commit_pair(&accf[0]);
-        umma_commit_pair(&accf[1]);
+        *abort_flag = 1;
+        umma_commit_pair(&accf[buf]);
       }
     }
     __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ scales (both CTAs)
+    const bool va = (a.ldsa & 3) == 0 && (reinterpret_cast<uintptr_t>(a.sa) & 15) == 0;
+    const bool vb = (a.ldsb & 3) == 0 && (reinterpret_cast<uintptr_t>(a.sb) & 15) == 0;
+    int slot = 0;
+    uint32_t ph = 1;
+    bool go = true, wrapped = false;
+    for (int64_t t = blockIdx.x >> 1; go && t < tiles; t += step) {
+      const int m0 = (int)(t / nt) * 256 + 128 * (int)rank, n0 = (int)(t % nt) * 256;
+      for (int b = 0; b < a.nkb; b += 4) {
+        if (wrapped && !__all_sync(0xffffffffu, mbar_wait(&sce[slot], ph, a.err))) {
+          go = false;
+          break;
+        }
+        float* dst = scales + slot * kSlotFloats;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int r = 32 * i + lane, m = m0 + r;
+          copy_scales(dst + 4 * r, a.sa + (int64_t)(m < a.M ? m : 0) * a.ldsa, b, a.nkb, m < a.M, va);
+        }
+        if constexpr (BROW) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int r = 32 * i + lane, n = n0 + r;
+            copy_scales(dst + 512 + 4 * r, a.sb + (int64_t)(n < a.N ? n : 0) * a.ldsb, b, a.nkb, n < a.N, vb);
+          }
+        } else if (lane < 2) {
+          const int n = n0 + 128 * lane;
+          copy_scales(dst + 512 + 4 * lane, a.sb + (int64_t)(n < a.N ? n >> 7 : 0) * a.ldsb, b, a.nkb, n < a.N, vb);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&scf[slot])) : "memory");
+        if (++slot == kSlots) slot = 0, ph ^= 1u, wrapped = true;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // this warp's copies have landed
   } else if (warp >= 4) {
     // ------------------------------------------------------------ totals and epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q = warp & 3;                // tensor-memory lane quadrant
     const int half = (warp >> 2) - 1;      // column half
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const uint32_t empty_bar[2] = {cluster_addr(&acce[0], 0), cluster_addr(&acce[1], 0)};
     uint8_t* box = boxes + (size_t)(warp - 4) * kBoxBytes;
-    const int ct = threadIdx.x - 128;      // 0..255
-    uint32_t ph = 0;
-    int buf = 0, sbuf = 0;
+    uint32_t ph = 0, sph = 0;
+    int buf = 0, slot = 0;
     bool ok = true, box_used = false;
     for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += step) {
       const int m0 = (int)(t / nt) * 256 + 128 * (int)rank, n0 = (int)(t % nt) * 256;
-      const int m = m0 + 32 * q + lane;
       const int nh = n0 + 128 * half;      // first column of this thread
-      const float* sa = a.sa + (int64_t)(m < a.M ? m : a.M - 1) * a.ldsa;
-      const int nb = nh < a.N ? nh >> 7 : 0;
-      const float* sb = BROW ? a.sb + (int64_t)(n0 + ct < a.N ? n0 + ct : a.N - 1) * a.ldsb : a.sb + (int64_t)nb * a.ldsb;
+      constexpr int kSa = BROW ? 4 : 1;    // rows of a thread
+      const int row0 = 32 * q + (BROW ? lane >> 2 : lane);
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      float sa_next = __ldg(sa), sb_next = __ldg(sb);
       for (int kb = 0; kb < a.nkb; ++kb) {
-        const float sav = sa_next, sbv = sb_next;
-        if constexpr (BROW) {
-          sb_row[sbuf * 256 + ct] = sbv;  // this half's readers have passed the last barrier
-          asm volatile("bar.sync 1, 256;" ::: "memory");
-        }
-        if (kb + 1 < a.nkb) sa_next = __ldg(sa + kb + 1), sb_next = __ldg(sb + kb + 1);
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&accf[buf], ph, a.err)) && !*abort_flag;
-        if (!ok && !BROW) break;  // BROW: every warp keeps meeting the barrier, to the end of the tile
+        const int k4 = kb & 3;
+        if (k4 == 0) ok = __all_sync(0xffffffffu, mbar_wait(&scf[slot], sph, a.err));
+        const float* sc = scales + slot * kSlotFloats + k4;
+        float sav[kSa];
+#pragma unroll
+        for (int i = 0; i < kSa; ++i) sav[i] = sc[4 * (row0 + 8 * i)];
+        sc += 512;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&accf[buf], ph, a.err));
+        if (!ok) break;
         tc_fence_after();
-        if (ok) {
-          const float2 f = dup2(BROW ? sav : sav * sbv);
-          const float* sr = sb_row + sbuf * 256 + 128 * half;
+        const uint32_t src = tmem + lanes + 256u * buf + 128u * half;
+        uint32_t p[2][BROW ? 16 : 32];
+        auto release = [&] {  // the accumulator is read: its next block may start
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(empty_bar[buf]);
+        };
+        if constexpr (BROW) {
+          // fragments: a thread has four rows and 32 columns, so that it reads 32 of B's scales and not
+          // 128 (one row and 128 columns a thread: 1024 cycles a block for the reads alone, 270 us at
+          // 5120 x 5120 x 4096; so: see below)
+          const float* sr = sc + 4 * (128 * half + 2 * (lane & 3));
+          auto at = [&](int c) { return src + ((uint32_t)(c & 1) << 20) + 32u * (c >> 1); };  // chunk c: 16 rows x 32 columns
+          tmem_ld16x32_issue(at(0), p[0]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float2 p[8];
-            tmem_ld16(tmem + lanes + 256u * buf + 128u * half + 16u * c, p);
+          for (int c = 0; c < 8; ++c) {  // chunk c + 1 is on its way while chunk c is added
+            const uint32_t(&v)[16] = p[c & 1];
+            tmem_ld_wait(p[c & 1]);
+            if (c < 7) tmem_ld16x32_issue(at(c + 1), p[(c + 1) & 1]);
+            else release();
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              if constexpr (BROW) {
-                const float4 s4 = *reinterpret_cast<const float4*>(sr + 16 * c + 2 * i);
-                acc[8 * c + i] = fma2(p[i], mul2(f, make_float2(s4.x, s4.y)), acc[8 * c + i]);
-                acc[8 * c + i + 1] = fma2(p[i + 1], mul2(f, make_float2(s4.z, s4.w)), acc[8 * c + i + 1]);
-              } else {
-                acc[8 * c + i] = fma2(p[i], f, acc[8 * c + i]);
-                acc[8 * c + i + 1] = fma2(p[i + 1], f, acc[8 * c + i + 1]);
+            for (int jj = 0; jj < 4; ++jj) {
+              const int o = 4 * (32 * (c >> 1) + 8 * jj);
+              const float2 s2 = make_float2(sr[o], sr[o + 4]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float2* t = acc + 32 * (c & 1) + 8 * (c >> 1) + 2 * jj + h;
+                *t = fma2(make_float2(__uint_as_float(v[4 * jj + 2 * h]), __uint_as_float(v[4 * jj + 2 * h + 1])),
+                          mul2(s2, dup2(sav[2 * (c & 1) + h])), *t);
               }
             }
           }
+        } else {
+          const float2 f = dup2(sav[0] * sc[4 * half]);
+          auto add = [&](const uint32_t (&v)[32], int c) {  // the totals of columns 32 c.. of the half
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              acc[16 * c + i] = fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f, acc[16 * c + i]);
+          };
+          tmem_ld32_issue(src, p[0]);
+          tmem_ld32_issue(src + 32, p[1]);
+          tmem_ld_wait(p[0], p[1]);
+          add(p[0], 0);
+          tmem_ld32_issue(src + 64, p[0]);
+          add(p[1], 1);
+          tmem_ld32_issue(src + 96, p[1]);
+          tmem_ld_wait(p[0], p[1]);
+          release();
+          add(p[0], 2);
+          add(p[1], 3);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(empty_bar[buf]);
         if (++buf == 2) buf = 0, ph ^= 1u;
-        sbuf ^= 1;
+        if (k4 == 3 || kb == a.nkb - 1) {  // the group of scales has been read
+          __syncwarp();
+          if (lane == 0) mbar_arrive1(&sce[slot]);
+          if (++slot == kSlots) slot = 0, sph ^= 1u;
+        }
       }
       if (!ok) break;
       // bias, activation, and the way out: boxes of 128 bytes x 32 rows in shared memory (128-byte
@@ -296,23 +433,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
           }
-          uint8_t* row = box + lane * 128;
+          auto bias = [&](int n) { return a.d && n < a.N ? __ldg(a.d + n) : 0.0f; };
+          if constexpr (BROW) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            constexpr int kE = kCols / 8;  // elements of a 16-byte chunk
-            float o[kE];
+            for (int jj = 0; jj < kCols / 8; ++jj) {
+              const int c = 8 * jj + 2 * (lane & 3);  // column of the box
+              const float d0 = bias(col0 + c), d1 = bias(col0 + c + 1);
 #pragma unroll
-            for (int e = 0; e < kE; e += 2) {
-              const float2 v = acc[(b * kCols + c * kE + e) / 2];
-              const int n = col0 + c * kE + e;
-              o[e] = v.x + (a.d && n < a.N ? __ldg(a.d + n) : 0.0f);
-              o[e + 1] = v.y + (a.d && n + 1 < a.N ? __ldg(a.d + n + 1) : 0.0f);
-              if constexpr (!F32) o[e] = f8_act<EPI>(o[e]), o[e + 1] = f8_act<EPI>(o[e + 1]);
+              for (int i = 0; i < 4; ++i) {
+                const int cb = b * kCols + 8 * jj;  // column of the half
+                const float2 v = acc[32 * (i >> 1) + 16 * (cb >> 6) + 2 * ((cb & 63) >> 3) + (i & 1)];
+                const int r = (lane >> 2) + 8 * i;
+                const float o0 = f8_act<EPI>(v.x + d0), o1 = f8_act<EPI>(v.y + d1);
+                constexpr int kEs = F32 ? 4 : 2;
+                uint8_t* at = box + r * 128 + ((((c * kEs) >> 4) ^ (r & 7)) << 4) + ((c * kEs) & 15);
+                if constexpr (F32) *reinterpret_cast<float2*>(at) = make_float2(o0, o1);
+                else *reinterpret_cast<uint32_t*>(at) = Vec<__nv_bfloat16>::join(o0, o1);
+              }
             }
-            uint4 w;
-            if constexpr (F32) w = Vec<float>::pack(o);
-            else w = Vec<__nv_bfloat16>::pack(o);
-            *reinterpret_cast<uint4*>(row + ((c ^ (lane & 7)) << 4)) = w;
+          } else {
+            uint8_t* row = box + lane * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              constexpr int kE = kCols / 8;  // elements of a 16-byte chunk
+              float o[kE];
+#pragma unroll
+              for (int e = 0; e < kE; e += 2) {
+                const float2 v = acc[(b * kCols + c * kE + e) / 2];
+                const int n = col0 + c * kE + e;
+                o[e] = f8_act<EPI>(v.x + bias(n));
+                o[e + 1] = f8_act<EPI>(v.y + bias(n + 1));
+              }
+              uint4 w;
+              if constexpr (F32) w = Vec<float>::pack(o);
+              else w = Vec<__nv_bfloat16>::pack(o);
+              *reinterpret_cast<uint4*>(row + ((c ^ (lane & 7)) << 4)) = w;
+            }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
