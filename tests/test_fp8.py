@@ -78,7 +78,7 @@ def same_codes(a, b):
 
 # ---------------------------------------------------------------- norm + quantise
 
-ROWS = [(1, 5120), (3, 64), (5, 128), (7, 200), (2, 77), (33, 1000), (4, 1), (130, 1288), (2, 8192), (600, 384)]
+ROWS = [(1, 5120), (3, 64), (5, 128), (7, 200), (2, 77), (33, 1000), (4, 1), (130, 1288), (2, 8192), (600, 384), (200, 2000), (5, 513), (160, 5120)]
 
 
 @pytest.mark.gpu
@@ -120,6 +120,15 @@ def test_norm_quant(gpu, rows, hidden, dt, norm, gemma, act):
     slack = 1e-5 * (mag + (z.abs() if act != "none" else 0)) * (1 + (mu * rs).abs() if norm == "ln" else 1)
     check_codes(q, s, v, slack, "norm_quant")
     assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
+def test_norm_quant_parameters_off_16_bytes(gpu):
+    x = torch.randn(9, 520, device="cuda").bfloat16()
+    w, b = (torch.randn(523, device="cuda").bfloat16() for _ in range(2))
+    got = gn.norm_quant_fp8(x, w[3:], b[1:521], 1e-5, norm="ln", epilogue="silu")
+    want = gn.norm_quant_fp8(x, w[3:].clone(), b[1:521].clone(), 1e-5, norm="ln", epilogue="silu")
+    assert same_codes(got[0], want[0]) and all(torch.equal(p, q) for p, q in zip(got[1:], want[1:]))
 
 
 # ---------------------------------------------------------------- matrices, both ways

@@ -155,8 +155,10 @@ def _ptr(t):
 
 
 def _stream(stream=None) -> int:
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    return (stream or torch.cuda.current_stream()).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _epi(epi) -> int:
@@ -210,8 +212,10 @@ def empty_rows(shape, dtype, device):
     torch = _torch()
     shape = tuple(shape)
     hidden = shape[-1]
-    es = torch.empty((), dtype=dtype).element_size()
+    es = dtype.itemsize
     ld = (hidden * es + 15) // 16 * 16 // es
+    if ld == hidden:
+        return torch.empty(shape, dtype=dtype, device=device)
     rows = 1
     for n in shape[:-1]:
         rows *= n
@@ -566,10 +570,9 @@ def groupnorm_fwd(x, groups, w=None, b=None, eps=1e-5, epilogue="none", out=None
     y = empty_rows(x.shape, x.dtype, x.device) if out is None else out
     _need(y, "out", like=x, shape=x.shape, contiguous=False)
     _, _, _, ldy = _images(y, "out", like=x, dtype=x.dtype)
-    mk = (lambda: torch.empty((N, groups), dtype=torch.float32, device=x.device))
-    mu, rs = (mk(), mk()) if save_stats else (None, None)
+    mu, rs = torch.empty((2, N, groups), dtype=torch.float32, device=x.device).unbind(0) if save_stats else (None, None)
     nws = gn_groupnorm_fwd_workspace(N, S, Cn, groups, _dt(x))
-    ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=x.device)
+    ws = torch.empty(nws, dtype=torch.uint8, device=x.device) if nws else None
     check(gn_groupnorm_fwd(_ptr(x), _ptr(w), _ptr(b), _ptr(y), _ptr(mu), _ptr(rs), _ptr(ws), nws, N, S, Cn, groups, ld,
                            ldy, eps, _epi(epilogue), _dt(x), _stream(stream)), "gn_groupnorm_fwd")
     return y, mu, rs
@@ -588,10 +591,9 @@ def groupnorm_bwd(x, groups, w, b, mean, rstd, dy, epilogue="none", want_wgrad=T
     _, _, _, lddy = _images(dy, "dy", like=x, dtype=x.dtype)
     dx = empty_rows(x.shape, x.dtype, x.device)
     _, _, _, lddx = _images(dx)
-    mk = (lambda: torch.empty(Cn, dtype=torch.float32, device=x.device))
-    dw, db = (mk(), mk()) if want_wgrad else (None, None)
+    dw, db = torch.empty((2, Cn), dtype=torch.float32, device=x.device).unbind(0) if want_wgrad else (None, None)
     nws = gn_groupnorm_bwd_workspace(N, S, Cn, groups, _dt(x))
-    ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=x.device)
+    ws = torch.empty(nws, dtype=torch.uint8, device=x.device) if nws else None
     check(gn_groupnorm_bwd(_ptr(x), _ptr(w), _ptr(b), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(db),
                            _ptr(ws), nws, N, S, Cn, groups, ld, lddy, lddx, _epi(epilogue), _dt(x), _stream(stream)),
           "gn_groupnorm_bwd")
@@ -606,8 +608,8 @@ def _blocks(n):
 
 
 def _codes(rows, cols, device):
-    torch = _torch()
-    return empty_rows((rows, cols), torch.float8_e4m3fn, device)
+    """uninitialised codes [rows, cols] and their row stride"""
+    return empty_rows((rows, cols), _torch().float8_e4m3fn, device), (cols + 15) // 16 * 16
 
 
 @_placed
@@ -620,12 +622,14 @@ def norm_quant_fp8(x, g=None, beta=None, eps=1e-6, norm="rms", gemma=False, epil
     kind = _norm(norm)
     _need(g, "g", like=x, shape=(hidden,), dtype=x.dtype, optional=True)
     _need(beta, "beta", like=x, shape=(hidden,), dtype=x.dtype, optional=True)
-    q = _codes(rows, hidden, x.device)
-    s = torch.empty((rows, _blocks(hidden)), dtype=torch.float32, device=x.device)
-    mu = torch.empty(rows, dtype=torch.float32, device=x.device) if save_stats and kind == GN_NORM_LN else None
-    rs = torch.empty(rows, dtype=torch.float32, device=x.device) if save_stats and kind != GN_NORM_NONE else None
+    f32, device = torch.float32, x.device
+    q, ldq = _codes(rows, hidden, device)
+    nb = _blocks(hidden)
+    s = torch.empty((rows, nb), dtype=f32, device=device)
+    mu = torch.empty(rows, dtype=f32, device=device) if save_stats and kind == GN_NORM_LN else None
+    rs = torch.empty(rows, dtype=f32, device=device) if save_stats and kind != GN_NORM_NONE else None
     check(gn_norm_quant_fp8(_ptr(x), _ptr(g), _ptr(beta), _ptr(q), _ptr(s), _ptr(mu), _ptr(rs), rows, hidden, ld,
-                            _rows16(q)[2], _ld(s), eps, kind, int(gemma), _epi(epilogue), _dt(x), _stream(stream)),
+                            ldq, nb, eps, kind, int(gemma), _epi(epilogue), _dt(x), _stream(stream)),
           "gn_norm_quant_fp8")
     return q, s, mu, rs
 
@@ -647,16 +651,16 @@ def _quant_fp8(x, dy, tile, by_rows, transposed, want_db, epilogue, stream=None)
         _need(dy, "dy", like=x, shape=x.shape, contiguous=False)
         _, _, lddy = _rows16(dy, "dy", like=x, dtype=x.dtype)
     mk = (lambda r, c: torch.empty((r, c), dtype=torch.float32, device=x.device))
-    q = _codes(rows, cols, x.device) if by_rows else None
-    s = mk(_blocks(rows) if tile else rows, _blocks(cols)) if by_rows else None
-    qt = _codes(cols, rows, x.device) if transposed else None
-    st = mk(_blocks(cols) if tile else cols, _blocks(rows)) if transposed else None
+    rb, cb = _blocks(rows), _blocks(cols)
+    q, ldq = _codes(rows, cols, x.device) if by_rows else (None, 0)
+    s = mk(rb if tile else rows, cb) if by_rows else None
+    qt, ldqt = _codes(cols, rows, x.device) if transposed else (None, 0)
+    st = mk(cb if tile else cols, rb) if transposed else None
     db = torch.empty(cols, dtype=torch.float32, device=x.device) if want_db else None
     nws = gn_quant_fp8_workspace(rows, cols) if want_db else 0
     ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=x.device) if want_db else None
     check(gn_quant_fp8(_ptr(x), _ptr(dy), _ptr(q), _ptr(s), _ptr(qt), _ptr(st), _ptr(db), _ptr(ws), nws, rows, cols, ld,
-                       lddy, 0 if q is None else _rows16(q)[2], 0 if s is None else _ld(s), 0 if qt is None else _rows16(qt)[2],
-                       0 if st is None else _ld(st), GN_FP8_TILE if tile else GN_FP8_VEC, _epi(epilogue), _dt(x),
+                       lddy, ldq, cb, ldqt, rb, GN_FP8_TILE if tile else GN_FP8_VEC, _epi(epilogue), _dt(x),
                        _stream(stream)), "gn_quant_fp8")
     return q, s, qt, st, db
 
@@ -690,10 +694,11 @@ def linear_fp8(a, sa, b, sb, d=None, epilogue="none", out=None, out_dtype=None, 
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
         raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} must be [M, K] and [N, K]")
     (M, K), N = a.shape, b.shape[0]
-    _need(sa, "sa", like=a, shape=(M, _blocks(K)), dtype=torch.float32, contiguous=False)
+    nb, kb = _blocks(N), _blocks(K)
+    _need(sa, "sa", like=a, shape=(M, kb), dtype=torch.float32, contiguous=False)
     _need(sb, "sb", like=a, dtype=torch.float32, contiguous=False)
-    if tuple(sb.shape) not in ((_blocks(N), _blocks(K)), (N, _blocks(K))):
-        raise ValueError(f"sb has shape {tuple(sb.shape)}, expected {(_blocks(N), _blocks(K))} or {(N, _blocks(K))}")
+    if tuple(sb.shape) not in ((nb, kb), (N, kb)):
+        raise ValueError(f"sb has shape {tuple(sb.shape)}, expected {(nb, kb)} or {(N, kb)}")
     for t, name in ((sa, "sa"), (sb, "sb")):
         if t.numel() and t.stride(-1) != 1 and t.shape[1] > 1:
             raise ValueError(f"last dimension of {name} must be contiguous")
@@ -707,7 +712,7 @@ def linear_fp8(a, sa, b, sb, d=None, epilogue="none", out=None, out_dtype=None, 
     _need(y, "out", like=a, shape=(M, N), contiguous=False)
     _, _, ldy = _rows16(y, "out", like=a, dtype=out_dtype or y.dtype)
     check(gn_linear_fp8(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(d), _ptr(y), M, N, K, lda, _ld(sa), ldb, _ld(sb),
-                        ldy, FP8_BLOCK if sb.shape[0] == _blocks(N) else 1, int(accumulate), _epi(epilogue), _dt(y),
+                        ldy, FP8_BLOCK if sb.shape[0] == nb else 1, int(accumulate), _epi(epilogue), _dt(y),
                         _stream(stream)), "gn_linear_fp8")
     return y
 
