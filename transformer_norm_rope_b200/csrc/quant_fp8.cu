@@ -43,27 +43,24 @@ __device__ __forceinline__ float inverse(float s) {
   return EXACT ? __frcp_rn(s) : __fdividef(1.0f, s);
 }
 
-// v / s for a value that is itself an fp32 evaluation (EXACT false): one rounding of 1 / s more is no
-// more than what v already carries
-template <bool EXACT>
-__device__ __forceinline__ float scaled(float v, float s, float i) {
-  return EXACT ? quotient(v, s, i) : v * i;
-}
-
 // two codes, lo in the low byte
 __device__ __forceinline__ uint32_t code2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// four codes of v / s, i = 1 / s. EXACT: the rounded quotient; otherwise v i, for values that are themselves
+// fp32 evaluations: one rounding more is no more than they already carry.
 template <bool EXACT>
 __device__ __forceinline__ uint32_t code4(const float* v, float s, float i) {
-  if constexpr (!EXACT) {
-    const float2 lo = mul2(make_float2(v[0], v[1]), dup2(i)), hi = mul2(make_float2(v[2], v[3]), dup2(i));
-    return code2(lo.x, lo.y) | code2(hi.x, hi.y) << 16;
+  const float2 a = make_float2(v[0], v[1]), b = make_float2(v[2], v[3]), ii = dup2(i);
+  float2 lo = mul2(a, ii), hi = mul2(b, ii);
+  if constexpr (EXACT) {  // the quotient's last step, on pairs
+    const float2 ns = dup2(-s);
+    lo = fma2(fma2(lo, ns, a), ii, lo);
+    hi = fma2(fma2(hi, ns, b), ii, hi);
   }
-  return code2(scaled<EXACT>(v[0], s, i), scaled<EXACT>(v[1], s, i)) |
-         code2(scaled<EXACT>(v[2], s, i), scaled<EXACT>(v[3], s, i)) << 16;
+  return code2(lo.x, lo.y) | code2(hi.x, hi.y) << 16;
 }
 
 // The activation and its derivative for values on their way to codes. The hardware tanh (error 2^-11) of
@@ -158,17 +155,171 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int v, int n, const fl
 }
 
 // ---------------------------------------------------------------- norm + quantise, blocks along the row
-// The row is read once and stays in registers, VPT vectors a thread: statistics (mean, then centred
-// squares), normalise, activate, then each run of 128 / E threads holds a block of 128 values, finds its
-// amax with shuffles and writes the codes. A row belongs to the warps of one block (TEAM of blockDim.x
-// threads) or, up to 128 vectors, to one warp of eight (TEAM 32, no barrier). Bound by HBM: 3 bytes a
-// value in and out for bf16.
-template <typename T, int NORM, int EPI, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : VPT == 4 ? 512 : 1024) norm_quant_kernel(const T* __restrict__ x, const T* __restrict__ g,
+// The row is read once and stays in registers: statistics, then normalise, activate, and each run of
+// 128 / E lanes holds a block of 128 values, finds its amax with shuffles and writes the codes. Bound by HBM
+// (3 bytes a value in and out for bf16) only if the instructions stay near ten a value, so what a row
+// costs once should be paid by few threads:
+//   * norm_quant_warp_kernel, rows of up to 640 vectors: one warp per row, VPT vectors a lane kept packed,
+//     the parameters in shared memory, one block of sixteen warps per SM (two while rows are short).
+//   * norm_quant_row_kernel: one block per row, for longer rows and while there are too few rows to fill
+//     the SMs, where a row's latency counts.
+template <int VPT>
+constexpr int kWarpRows = VPT > 12 ? 12 : 16;  // warps of a block: 168 registers a thread for 80 of packed row
+
+// the packed vectors are unpacked again after this, not kept unpacked in twice the registers
+template <int N>
+__device__ __forceinline__ void keep_packed(uint4 (&u)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) asm volatile("" : "+r"(u[k].x), "+r"(u[k].y), "+r"(u[k].z), "+r"(u[k].w));
+}
+
+template <typename T, int NORM, int EPI, int VPT>
+__global__ void __launch_bounds__(32 * kWarpRows<VPT>, VPT <= 4 ? 2 : 1)
+    norm_quant_warp_kernel(const T* __restrict__ x, const T* __restrict__ g, const T* __restrict__ beta,
+                           uint8_t* __restrict__ q, float* __restrict__ scale, float* __restrict__ mean,
+                           float* __restrict__ rstd, int64_t rows, int hidden, int64_t ldx, int64_t ldq, int64_t lds,
+                           float eps, int gemma) {
+  constexpr int E = Vec<T>::N, H = E / 2;
+  constexpr int L = kBlk / E;  // lanes of a block of values
+  constexpr bool FAST = fast_math_for<T>();
+  constexpr bool EXACT = NORM == GN_NORM_NONE && EPI == EPI_NONE;
+  constexpr int kGroup = VPT < 4 ? VPT : 4;  // vectors whose scales are made together
+  static_assert(VPT % kGroup == 0 && (VPT < 4 ? VPT != 3 : true), "groups of vectors");
+  extern __shared__ uint4 params[];  // [1 or 2][32 VPT] vectors: weight, bias
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if constexpr (NORM != GN_NORM_NONE) {
+    for (int v = threadIdx.x; v < 32 * VPT; v += 32 * kWarpRows<VPT>) {
+      float w[E], b[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        w[e] = v * E + e < hidden ? ld_param(g, v * E + e, 1.0f) : 0.0f;
+        b[e] = NORM == GN_NORM_LN && v * E + e < hidden ? ld_param(beta, v * E + e, 0.0f) : 0.0f;
+      }
+      params[v] = Vec<T>::pack(w);
+      if (NORM == GN_NORM_LN) params[32 * VPT + v] = Vec<T>::pack(b);
+    }
+    __syncthreads();
+  }
+  const float inv_n = 1.0f / (float)hidden;
+  const float2 gem = dup2(NORM == GN_NORM_RMS && gemma ? 1.0f : 0.0f);
+  const bool aligned = hidden % E == 0, full = hidden == 32 * VPT * E;
+  for (int64_t m = (int64_t)blockIdx.x * kWarpRows<VPT> + warp; m < rows; m += (int64_t)gridDim.x * kWarpRows<VPT>) {
+    const T* row = x + m * ldx;
+    uint4 raw[VPT];
+    if (aligned) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        raw[k] = make_uint4(0, 0, 0, 0);
+        if ((lane + 32 * k) * E < hidden) raw[k] = ld_stream(row + (lane + 32 * k) * E);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) raw[k] = load_raw<T>(row, lane + 32 * k, hidden);
+    }
+    float mu = 0.0f, r = 1.0f;
+    if constexpr (NORM == GN_NORM_RMS) {
+      float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        float2 f[H];
+        unpack2<T>(raw[k], f);
+#pragma unroll
+        for (int e = 0; e < H; ++e) acc = fma2(f[e], f[e], acc);
+      }
+      r = rsqrtf(fmaf(group_sum<32>(acc.x + acc.y), inv_n, eps));
+    } else if constexpr (NORM == GN_NORM_LN) {
+      float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        float2 f[H];
+        unpack2<T>(raw[k], f);
+#pragma unroll
+        for (int e = 0; e < H; ++e) acc = add2(acc, f[e]);
+      }
+      mu = group_sum<32>(acc.x + acc.y) * inv_n;
+      acc = make_float2(0.0f, 0.0f);
+      keep_packed(raw);
+      if (full) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          float2 f[H];
+          unpack2<T>(raw[k], f);
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            const float2 d = add2(f[e], dup2(-mu));
+            acc = fma2(d, d, acc);
+          }
+        }
+      } else {  // some of the lanes' values lie past the row
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          float2 f[H];
+          unpack2<T>(raw[k], f);
+          const int left = hidden - (lane + 32 * k) * E;  // elements of the row from this vector on
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            const float2 d = add2(f[e], dup2(-mu));
+            acc = fma2(d, make_float2(2 * e < left ? d.x : 0.0f, 2 * e + 1 < left ? d.y : 0.0f), acc);
+          }
+        }
+      }
+      r = rsqrtf(fmaf(group_sum<32>(acc.x + acc.y), inv_n, eps));
+    }
+    if constexpr (NORM != GN_NORM_NONE) {
+      keep_packed(raw);
+      if (lane == 0) {
+        if (mean && NORM == GN_NORM_LN) mean[m] = mu;
+        if (rstd) rstd[m] = r;
+      }
+    }
+#pragma unroll
+    for (int k0 = 0; k0 < VPT; k0 += kGroup) {
+      if (32 * k0 * E >= hidden) break;
+      float f[kGroup][E];
+      float am[kGroup];
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) {
+        const int v = lane + 32 * (k0 + j);
+        float2 z[H];
+        unpack2<T>(raw[k0 + j], z);
+        if constexpr (NORM != GN_NORM_NONE) {
+          float2 w[H], b[H];
+          unpack2<T>(params[v], w);
+          if constexpr (NORM == GN_NORM_LN) unpack2<T>(params[32 * VPT + v], b);
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            if constexpr (NORM == GN_NORM_LN) z[e] = fma2(mul2(add2(z[e], dup2(-mu)), dup2(r)), w[e], b[e]);
+            else z[e] = mul2(mul2(z[e], dup2(r)), add2(w[e], gem));
+          }
+        }
+        am[j] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          f[j][2 * e] = EPI == EPI_NONE ? z[e].x : q_act<EPI, FAST>(z[e].x);
+          f[j][2 * e + 1] = EPI == EPI_NONE ? z[e].y : q_act<EPI, FAST>(z[e].y);
+          am[j] = max_nan(am[j], max_nan(fabsf(f[j][2 * e]), fabsf(f[j][2 * e + 1])));
+        }
+      }
+      // each lane makes the scale of one of its group's blocks
+      const float s = block_scale(group_max<kGroup, L>(am, lane)), i = inverse<EXACT>(s);
+      const int vs = lane + 32 * (k0 + value_of_lane<kGroup, L>(lane));
+      if (lane % (L / kGroup) == 0 && vs / L * kBlk < hidden) scale[m * lds + vs / L] = s;
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) {
+        const int v = lane + 32 * (k0 + j), src = lane_of_value<kGroup, L>(lane, j);
+        const float ij = __shfl_sync(0xffffffffu, i, src), sj = EXACT ? __shfl_sync(0xffffffffu, s, src) : 0.0f;
+        if (v * E < hidden) store_codes<E, EXACT>(q + m * ldq, v, hidden, f[j], sj, ij);
+      }
+    }
+  }
+}
+
+template <typename T, int NORM, int EPI, int VPT>
+__global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_quant_row_kernel(const T* __restrict__ x, const T* __restrict__ g,
                                                                        const T* __restrict__ beta,
                                                                        uint8_t* __restrict__ q, float* __restrict__ scale,
                                                                        float* __restrict__ mean, float* __restrict__ rstd,
-                                                                       int64_t rows, int hidden, int64_t ldx, int64_t ldq,
+                                                                       int hidden, int64_t ldx, int64_t ldq,
                                                                        int64_t lds, float eps, int gemma, int pvec) {
   constexpr int E = Vec<T>::N;
   constexpr int L = kBlk / E;  // threads of a block of values
@@ -176,10 +327,9 @@ __global__ void __launch_bounds__(WARP ? 256 : VPT == 4 ? 512 : 1024) norm_quant
   constexpr bool EXACT = NORM == GN_NORM_NONE && EPI == EPI_NONE;
   __shared__ float red[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t m = WARP ? (int64_t)blockIdx.x * 8 + warp : (int64_t)blockIdx.x;
-  if (WARP && m >= rows) return;
-  const int t = WARP ? lane : threadIdx.x;
-  const int team = WARP ? 32 : (int)blockDim.x;
+  const int64_t m = blockIdx.x;
+  const int t = threadIdx.x;
+  const int team = (int)blockDim.x;
   const T* row = x + m * ldx;
   const bool ragged = (team * VPT) * E != hidden;  // some of the threads' values lie past the row
   uint4 raw[VPT];
@@ -198,24 +348,20 @@ __global__ void __launch_bounds__(WARP ? 256 : VPT == 4 ? 512 : 1024) norm_quant
   for (int k = 0; k < VPT; ++k) Vec<T>::unpack(raw[k], f[k]);
   auto total = [&](float v, int slot) {  // over the row's threads, in a fixed order
     v = group_sum<32>(v);
-    if constexpr (!WARP) {
-      if (lane == 0) red[slot][warp] = v;
-      __syncthreads();
-      v = lane < (int)(blockDim.x >> 5) ? red[slot][lane] : 0.0f;
-      v = group_sum<32>(v);
-    }
-    return v;
+    if (lane == 0) red[slot][warp] = v;
+    __syncthreads();
+    return group_sum<32>(lane < (int)(blockDim.x >> 5) ? red[slot][lane] : 0.0f);
   };
   float mu = 0.0f, r = 1.0f;
   if constexpr (NORM != GN_NORM_NONE) {
-    const float n = (float)hidden;
+    const float inv_n = 1.0f / (float)hidden;
     float2 acc = make_float2(0.0f, 0.0f);
     if constexpr (NORM == GN_NORM_LN) {
 #pragma unroll
       for (int k = 0; k < VPT; ++k)
 #pragma unroll
         for (int e = 0; e < E; e += 2) acc = add2(acc, make_float2(f[k][e], f[k][e + 1]));
-      mu = __fdiv_rn(total(acc.x + acc.y, 0), n);
+      mu = total(acc.x + acc.y, 0) * inv_n;
       acc = make_float2(0.0f, 0.0f);
     }
 #pragma unroll
@@ -232,7 +378,7 @@ __global__ void __launch_bounds__(WARP ? 256 : VPT == 4 ? 512 : 1024) norm_quant
         acc = fma2(d, d, acc);
       }
     }
-    r = __frcp_rn(__fsqrt_rn(__fdiv_rn(total(acc.x + acc.y, 1), n) + eps));
+    r = rsqrtf(fmaf(total(acc.x + acc.y, 1), inv_n, eps));
     if (t == 0) {
       if (mean && NORM == GN_NORM_LN) mean[m] = mu;
       if (rstd) rstd[m] = r;
@@ -299,15 +445,15 @@ __global__ void __launch_bounds__(WARP ? 256 : VPT == 4 ? 512 : 1024) norm_quant
 }
 
 // ---------------------------------------------------------------- tiles of 128 x 128
-// One block per tile: v = x, or dy * act'(x) (GRAD), read once, 64 values a thread in registers. Warp w
-// has the rows 16 w..: for bf16 a thread has 8 consecutive rows (lanes 0-15 the first eight of the warp's
-// 16, lanes 16-31 the others) x 8 columns, for fp32 all 16 rows x 4 columns. So a row's block is a run of
+// One block per tile: v = x, or dy * act'(x) (GRAD), read once, 32 values a thread in registers. Warp w
+// has the rows 8 w..: for bf16 a thread has 4 consecutive rows (lanes 0-15 the first four of the warp's
+// eight, lanes 16-31 the others) x 8 columns, for fp32 all 8 rows x 4 columns. So a row's block is a run of
 // lanes (amax by shuffles, codes stored from registers, 128 bytes a row), and a column's is the warp's
-// rows and then the eight warps (shared memory). The transposed codes of a thread are R consecutive bytes
-// of each of its columns: they meet in a 16 KiB byte tile (16-byte chunk j of column c at j ^ key(c), so
-// that neither side conflicts) and leave as 128-byte runs. Both ways and the bias gradient in one read:
+// rows and then the sixteen warps (shared memory). The transposed codes of a thread are R consecutive
+// bytes of each of its columns: they meet in a 16 KiB byte tile (16-byte chunk j of column c at j ^ key(c),
+// so that neither side conflicts) and leave as 128-byte runs. Both ways and the bias gradient in one read:
 // 6 bytes a value for a bf16 gradient. Bound by HBM.
-constexpr int kTileThreads = 256;
+constexpr int kTileThreads = 512, kTileWarps = 16;
 
 struct QuantArgs {
   const void* x;
@@ -324,18 +470,18 @@ template <typename T, int EPI, bool GRAD, bool TILE>
 __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const QuantArgs a) {
   constexpr int E = Vec<T>::N;
   constexpr int L = kBlk / E;         // lanes of a row: 16 or 32
-  constexpr int R = 64 / E;           // rows of a thread: 8 or 16
+  constexpr int R = 32 / E;           // rows of a thread: 4 or 8
   constexpr bool FAST = fast_math_for<T>();
   constexpr bool EXACT = !GRAD || EPI == EPI_NONE;
   __shared__ __align__(16) uint8_t bytes[kBlk * kBlk];
-  __shared__ float red_max[8][kBlk], red_sum[GRAD ? 8 : 1][kBlk];
+  __shared__ __align__(16) float red_max[kTileWarps][kBlk], red_sum[GRAD ? kTileWarps : 1][kBlk];
   __shared__ __align__(16) float col_scale[kBlk], col_inv[kBlk];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r0 = (int64_t)blockIdx.y * kBlk, c0 = (int64_t)blockIdx.x * kBlk;
   const int nr = a.rows - r0 < kBlk ? (int)(a.rows - r0) : kBlk;
   const int nc = a.cols - c0 < kBlk ? (int)(a.cols - c0) : kBlk;
   const int lv = lane % L;                          // vector of the row
-  const int row0 = 16 * warp + (lane / L) * R;      // first row of the thread
+  const int row0 = 8 * warp + (lane / L) * R;       // first row of the thread
   const T* x = static_cast<const T*>(a.x) + r0 * a.ldx + c0;
   const T* dy = GRAD ? static_cast<const T*>(a.dy) + r0 * a.lddy + c0 : nullptr;
   // whole tiles: every load of the thread is issued before the first value is used
@@ -390,29 +536,33 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
         if constexpr (GRAD) csum[e] += __shfl_xor_sync(0xffffffffu, csum[e], 16);
       }
     }
-    if (lane < L) {
+    if constexpr (TILE) {
+      float m = cmax[0];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        red_max[warp][lv * E + e] = cmax[e];
-        if constexpr (GRAD) red_sum[warp][lv * E + e] = csum[e];
+      for (int e = 1; e < E; ++e) m = max_nan(m, cmax[e]);
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (lane == 0) red_max[0][warp] = m;
+    } else if (lane < L) {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        *reinterpret_cast<float4*>(&red_max[warp][lv * E + e]) = make_float4(cmax[e], cmax[e + 1], cmax[e + 2], cmax[e + 3]);
+        if constexpr (GRAD)
+          *reinterpret_cast<float4*>(&red_sum[warp][lv * E + e]) = make_float4(csum[e], csum[e + 1], csum[e + 2], csum[e + 3]);
       }
     }
     __syncthreads();
     if constexpr (TILE) {
-      float m = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-#pragma unroll
-        for (int w = 0; w < 8; ++w) m = max_nan(m, red_max[w][lane + 32 * k]);
+      for (int w = 0; w < kTileWarps; w += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(&red_max[0][w]);
+        all = max_nan(all, max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w)));
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      all = m;
     } else if (a.qt) {  // a thread per column makes its scale
       if (threadIdx.x < kBlk) {
         float m = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) m = max_nan(m, red_max[w][threadIdx.x]);
+        for (int w = 0; w < kTileWarps; ++w) m = max_nan(m, red_max[w][threadIdx.x]);
         const float s = block_scale(m);
         col_scale[threadIdx.x] = s;
         col_inv[threadIdx.x] = inverse<EXACT>(s);
@@ -423,7 +573,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
       if (a.colsum && threadIdx.x < nc) {
         float t = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) t += red_sum[w][threadIdx.x];
+        for (int w = 0; w < kTileWarps; ++w) t += red_sum[w][threadIdx.x];
         a.colsum[(int64_t)blockIdx.y * a.cols + c0 + threadIdx.x] = t;
       }
     }
@@ -433,44 +583,85 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
     if (a.q) a.scale[(int64_t)blockIdx.y * a.lds + blockIdx.x] = s_all;
     if (a.qt) a.scale_t[(int64_t)blockIdx.x * a.ldst + blockIdx.y] = s_all;
   }
-  if (a.q) {
-    float s = s_all, inv = i_all;
-    if constexpr (!TILE) {  // each lane makes the scale of one of its group's rows
-      s = block_scale(group_max<R, L>(rmax, lane));
-      inv = inverse<EXACT>(s);
-      const int i = row0 + value_of_lane<R, L>(lane);
-      if (lane % (L / R) == 0 && i < nr) a.scale[(r0 + i) * a.lds + blockIdx.x] = s;
-    }
+  // where R codes of column c (vector lv of the row) go: chunk row / 16 of the column; its 8-byte halves change
+  // places on every other eight vectors
+  auto put = [&](int c, const uint32_t* w) {
+    uint8_t* at = bytes + c * kBlk + (((warp >> 1) ^ (lv & 7)) << 4) + 8 * ((warp & 1) ^ ((lv >> 3) & 1));
+    if constexpr (R == 4) *reinterpret_cast<uint32_t*>(at + 4 * (lane / L)) = w[0];
+    else *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+  };
+  if constexpr (TILE) {  // one scale: the codes are made once and their bytes transposed four by four
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int src = lane_of_value<R, L>(lane, i);
-      const float ii = TILE ? inv : __shfl_sync(0xffffffffu, inv, src);
-      const float si = TILE ? s : EXACT ? __shfl_sync(0xffffffffu, s, src) : 0.0f;
-      if (row0 + i < nr && lv * E < nc) store_codes<E, EXACT>(a.q + (r0 + row0 + i) * a.ldq + c0, lv, nc, f[i], si, ii);
+    for (int e = 0; e < E; e += 4) {
+      uint32_t w[R], t[4][R / 4];
+#pragma unroll
+      for (int i = 0; i < R; ++i) w[i] = code4<EXACT>(f[i] + e, s_all, i_all);
+      if (a.q) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int c = lv * E + e;
+          if (row0 + i >= nr || c >= nc) continue;
+          uint8_t* out = a.q + (r0 + row0 + i) * a.ldq + c0 + c;
+          if (c + 4 <= nc) {
+            *reinterpret_cast<uint32_t*>(out) = w[i];
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (c + k < nc) out[k] = (uint8_t)(w[i] >> (8 * k));
+          }
+        }
+      }
+      if (a.qt) {
+#pragma unroll
+        for (int k = 0; k < R / 4; ++k) {
+          const uint32_t *u = w + 4 * k;
+          const uint32_t p = __byte_perm(u[0], u[1], 0x5140), q = __byte_perm(u[2], u[3], 0x5140);
+          const uint32_t x = __byte_perm(u[0], u[1], 0x7362), y = __byte_perm(u[2], u[3], 0x7362);
+          t[0][k] = __byte_perm(p, q, 0x5410);
+          t[1][k] = __byte_perm(p, q, 0x7632);
+          t[2][k] = __byte_perm(x, y, 0x5410);
+          t[3][k] = __byte_perm(x, y, 0x7632);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) put(lv * E + e + k, t[k]);
+      }
+    }
+  } else {
+    if (a.q) {  // each lane makes the scale of one of its group's rows
+      const float s = block_scale(group_max<R, L>(rmax, lane)), inv = inverse<EXACT>(s);
+      const int ir = row0 + value_of_lane<R, L>(lane);
+      if (lane % (L / R) == 0 && ir < nr) a.scale[(r0 + ir) * a.lds + blockIdx.x] = s;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int src = lane_of_value<R, L>(lane, i);
+        const float ii = __shfl_sync(0xffffffffu, inv, src), si = EXACT ? __shfl_sync(0xffffffffu, s, src) : 0.0f;
+        if (row0 + i < nr && lv * E < nc) store_codes<E, EXACT>(a.q + (r0 + row0 + i) * a.ldq + c0, lv, nc, f[i], si, ii);
+      }
+    }
+    if (a.qt) {
+      __syncthreads();  // the columns' scales
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = lv * E + e;
+        const float s = EXACT ? col_scale[c] : 0.0f, inv = col_inv[c];
+        uint32_t w[R / 4];
+#pragma unroll
+        for (int k = 0; k < R / 4; ++k) {
+          const float v[4] = {f[4 * k][e], f[4 * k + 1][e], f[4 * k + 2][e], f[4 * k + 3][e]};
+          w[k] = code4<EXACT>(v, s, inv);
+        }
+        put(c, w);
+      }
     }
   }
   if (!a.qt) return;
-  if constexpr (!TILE) __syncthreads();  // the columns' scales
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int c = lv * E + e;
-    const float s = TILE ? s_all : EXACT ? col_scale[c] : 0.0f, inv = TILE ? i_all : col_inv[c];
-    uint32_t w[R / 4];
-#pragma unroll
-    for (int k = 0; k < R / 4; ++k) {
-      const float v[4] = {f[4 * k][e], f[4 * k + 1][e], f[4 * k + 2][e], f[4 * k + 3][e]};
-      w[k] = code4<EXACT>(v, s, inv);
-    }
-    uint8_t* at = bytes + c * kBlk + ((warp ^ (lv & 7)) << 4);
-    if constexpr (R == 8) *reinterpret_cast<uint2*>(at + 8 * (lane / L)) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
+  for (int it = 0; it < kBlk * 8 / kTileThreads; ++it) {
     const int idx = it * kTileThreads + threadIdx.x, c = idx >> 3, j = idx & 7;
     if (c >= nc || 16 * j >= nr) continue;
-    const uint4 v = *reinterpret_cast<const uint4*>(bytes + c * kBlk + ((j ^ ((c / E) & 7)) << 4));
+    uint4 v = *reinterpret_cast<const uint4*>(bytes + c * kBlk + ((j ^ ((c / E) & 7)) << 4));
+    if ((c / E) & 8) v = make_uint4(v.z, v.w, v.x, v.y);
     uint8_t* out = a.qt + (c0 + c) * a.ldqt + r0 + 16 * j;
     if (16 * j + 16 <= nr) {
       *reinterpret_cast<uint4*>(out) = v;
@@ -485,15 +676,20 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
 
 // ---------------------------------------------------------------- host side
 
-// variants of the row kernel: 0-2: one warp per row, 1, 2 or 4 vectors a lane; 3, 4: one block per row, 1
-// or 4 vectors a thread
+// shape > 0: one warp per row with that many vectors a lane; -1, -4: one block per row with 1 or 4 vectors
+// a thread
 template <typename T, int NORM, int EPI>
 void* pick_norm_shape(int shape) {
-  return shape == 0   ? (void*)norm_quant_kernel<T, NORM, EPI, 1, true>
-         : shape == 1 ? (void*)norm_quant_kernel<T, NORM, EPI, 2, true>
-         : shape == 2 ? (void*)norm_quant_kernel<T, NORM, EPI, 4, true>
-         : shape == 3 ? (void*)norm_quant_kernel<T, NORM, EPI, 1, false>
-                      : (void*)norm_quant_kernel<T, NORM, EPI, 4, false>;
+  switch (shape) {
+    case 1: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 1>;
+    case 2: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 2>;
+    case 4: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 4>;
+    case 8: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 8>;
+    case 12: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 12>;
+    case 20: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 20>;
+    case -1: return (void*)norm_quant_row_kernel<T, NORM, EPI, 1>;
+    default: return (void*)norm_quant_row_kernel<T, NORM, EPI, 4>;
+  }
 }
 template <typename T, int NORM>
 void* pick_norm_epi(int epi, int shape) {
@@ -537,24 +733,30 @@ extern "C" gn_status gn_norm_quant_fp8(const void* x, const void* g, const void*
   int pvec = (!g || aligned16(g)) && (!beta || aligned16(beta));  // parameters read 16 bytes at a time
   const int e = (int)(16 / dt_size(dt));
   const int nvec = (int)((hidden + e - 1) / e);
-  // up to 128 vectors: a warp per row; above, a block per row with four vectors a thread, or one while
-  // the rows do not fill the SMs anyway and the latency of a row counts
-  int shape, threads = 256;
-  int64_t blocks = (rows + 7) / 8;
-  if (nvec <= 128 && (rows > sm_count() || nvec <= 32)) {
-    shape = nvec <= 32 ? 0 : nvec <= 64 ? 1 : 2;
-  } else {
-    shape = nvec <= 1024 && rows <= sm_count() ? 3 : 4;
-    const int per = shape == 3 ? 1 : 4;
-    threads = ((nvec + per - 1) / per + 31) / 32 * 32;
-    blocks = rows;
-  }
-  void* kern = dt == GN_BF16 ? pick_norm<__nv_bfloat16>(norm, epi, shape) : pick_norm<float>(norm, epi, shape);
+  const int lanes = (nvec + 31) / 32;  // vectors a lane of a warp would hold
+  const int sms = sm_count() > 0 ? sm_count() : 148;
   int h = (int)hidden;
-  void* args[] = {&x, &g, &beta, &q, &scale, &mean, &rstd, &rows, &h, &ld_x, &ld_q, &ld_s, &eps, &gemma, &pvec};
-  if (!kernel_attrs(kern, 0)) return GN_ERR_CUDA;
-  if (cudaLaunchKernel(kern, dim3((unsigned)blocks), dim3((unsigned)threads), args, 0, (cudaStream_t)stream) != cudaSuccess)
-    return GN_ERR_CUDA;
+  if (lanes <= 20 && (lanes == 1 || rows > 4 * sms)) {
+    const int shape = lanes <= 2 ? lanes : lanes <= 4 ? 4 : lanes <= 8 ? 8 : lanes <= 12 ? 12 : 20;
+    void* kern = dt == GN_BF16 ? pick_norm<__nv_bfloat16>(norm, epi, shape) : pick_norm<float>(norm, epi, shape);
+    const size_t smem = norm == GN_NORM_NONE ? 0 : (size_t)(norm == GN_NORM_LN ? 2 : 1) * 32 * shape * 16;
+    const int warps = shape == 20 ? kWarpRows<20> : kWarpRows<1>;
+    const int most = persistent_grid(kern, 32 * warps, smem, 0);
+    if (most <= 0) return GN_ERR_CUDA;
+    const int64_t blocks = (rows + warps - 1) / warps;
+    void* args[] = {&x, &g, &beta, &q, &scale, &mean, &rstd, &rows, &h, &ld_x, &ld_q, &ld_s, &eps, &gemma};
+    if (cudaLaunchKernel(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3((unsigned)(32 * warps)), args, smem,
+                         (cudaStream_t)stream) != cudaSuccess)
+      return GN_ERR_CUDA;
+  } else {
+    const int per = nvec <= 1024 && rows <= sms ? 1 : 4;
+    void* kern = dt == GN_BF16 ? pick_norm<__nv_bfloat16>(norm, epi, -per) : pick_norm<float>(norm, epi, -per);
+    const int threads = ((nvec + per - 1) / per + 31) / 32 * 32;
+    void* args[] = {&x, &g, &beta, &q, &scale, &mean, &rstd, &h, &ld_x, &ld_q, &ld_s, &eps, &gemma, &pvec};
+    if (!kernel_attrs(kern, 0)) return GN_ERR_CUDA;
+    if (cudaLaunchKernel(kern, dim3((unsigned)rows), dim3((unsigned)threads), args, 0, (cudaStream_t)stream) != cudaSuccess)
+      return GN_ERR_CUDA;
+  }
   count_launches(1);
   return launch_status();
 }
