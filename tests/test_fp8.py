@@ -78,7 +78,7 @@ def same_codes(a, b):
 
 # ---------------------------------------------------------------- norm + quantise
 
-ROWS = [(1, 5120), (3, 64), (5, 128), (7, 200), (2, 77), (33, 1000), (4, 1), (130, 1288), (2, 8192), (600, 384), (200, 2000), (5, 513), (160, 5120)]
+ROWS = [(1, 5120), (3, 64), (5, 128), (7, 200), (2, 77), (33, 1000), (4, 1), (130, 1288), (2, 8192), (600, 384), (200, 2000), (5, 513), (160, 5120), (700, 5120), (650, 1291), (601, 8184)]
 
 
 @pytest.mark.gpu
@@ -120,6 +120,21 @@ def test_norm_quant(gpu, rows, hidden, dt, norm, gemma, act):
     slack = 1e-5 * (mag + (z.abs() if act != "none" else 0)) * (1 + (mu * rs).abs() if norm == "ln" else 1)
     check_codes(q, s, v, slack, "norm_quant")
     assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_norm_quant_rows_whose_beginning_is_far_off(gpu, dt):
+    """Statistics must not lose their bits to a first part of the row (or a mean) far from the rest."""
+    x = torch.randn(640, 5120)
+    x[::2, :256] += 500.0
+    x[1::4] += 300.0
+    x = x.to(DT[dt]).cuda()
+    _, _, mean, rstd = gn.norm_quant_fp8(x, norm="ln", eps=1e-5)
+    X = x.double()
+    mu, rs = X.mean(1), (X.var(1, correction=0) + 1e-5) ** -0.5
+    assert ((mean.double() - mu).abs() <= 4e-6 * (mu.abs() + 1 / rs)).all()
+    assert ((rstd.double() - rs).abs() <= 1e-5 * rs).all()
 
 
 @pytest.mark.gpu

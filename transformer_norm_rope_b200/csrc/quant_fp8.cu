@@ -11,6 +11,8 @@
 // nearest (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990, theorem on the last step of a division). Ties of bf16 values over a scale
 // derived from one of them are common, so a quotient one ulp off would flip codes.
+#include <type_traits>
+
 #include "gn_common.cuh"
 #include "gn_host.h"
 
@@ -66,31 +68,50 @@ __device__ __forceinline__ uint32_t code4(const float* v, float s, float i) {
 // The activation and its derivative for values on their way to codes. The hardware tanh (error 2^-11) of
 // the bf16 epilogues would move one code in a hundred; on bf16 inputs the exponential and the divide are the
 // approximate ones (together about 1e-6), on fp32 inputs the accurate ones.
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sigmoid(2 u) of the tanh-GeLU's argument: (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
+__device__ __forceinline__ float2 gelu_u2(float2 z, float2 z2) {  // -2 u log2(e)
+  return mul2(z, fma2(z2, dup2(-2.0f * kLog2e * kGeluK * kGeluC), dup2(-2.0f * kLog2e * kGeluK)));
+}
+
 template <int EPI, bool FAST>
-__device__ __forceinline__ float q_act(float z) {
+__device__ __forceinline__ float2 q_act2(float2 z) {
   if constexpr (!FAST || EPI == EPI_NONE) {
-    return epi_fwd<EPI, false>(z);
-  } else if constexpr (EPI == EPI_SILU) {
-    return __fdividef(z, 1.0f + __expf(-z));
-  } else {  // z (1 + tanh u) / 2 = z sigmoid(2 u)
-    const float u2 = z * fmaf(2.0f * kGeluK * kGeluC, z * z, 2.0f * kGeluK);
-    return __fdividef(z, 1.0f + __expf(-u2));
+    return make_float2(epi_fwd<EPI, false>(z.x), epi_fwd<EPI, false>(z.y));
+  } else {
+    const float2 t = EPI == EPI_SILU ? mul2(z, dup2(-kLog2e)) : gelu_u2(z, mul2(z, z));
+    const float2 d = add2(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), dup2(1.0f));
+    return mul2(z, make_float2(rcp_ftz(d.x), rcp_ftz(d.y)));
   }
 }
 template <int EPI, bool FAST>
-__device__ __forceinline__ float q_grad(float z) {
+__device__ __forceinline__ float2 q_grad2(float2 z) {
   if constexpr (!FAST || EPI == EPI_NONE) {
-    return epi_grad<EPI, false>(z);
-  } else if constexpr (EPI == EPI_SILU) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-z));
-    return s * fmaf(z, 1.0f - s, 1.0f);
-  } else {  // with p = sigmoid(2 u): p + z p (1 - p) (2 u)'; 1 - p = a / (1 + a) without cancellation
-    const float z2 = z * z;
-    const float u2 = z * fmaf(2.0f * kGeluK * kGeluC, z2, 2.0f * kGeluK);
-    const float a = __expf(-fabsf(u2));
-    const float r = __fdividef(1.0f, 1.0f + a), ra = r * a;
-    const float p = u2 >= 0.0f ? r : ra, n = u2 >= 0.0f ? ra : r;
-    return p * fmaf(z * n, fmaf(6.0f * kGeluK * kGeluC, z2, 2.0f * kGeluK), 1.0f);
+    return make_float2(epi_grad<EPI, false>(z.x), epi_grad<EPI, false>(z.y));
+  } else if constexpr (EPI == EPI_SILU) {  // s (1 + z (1 - s))
+    const float2 t = mul2(z, dup2(-kLog2e));
+    const float2 d = add2(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), dup2(1.0f));
+    const float2 s = make_float2(rcp_ftz(d.x), rcp_ftz(d.y));
+    return mul2(s, fma2(z, fma2(s, dup2(-1.0f), dup2(1.0f)), dup2(1.0f)));
+  } else {  // p = sigmoid(2 u): p (1 + z (1 - p) (2 u)'); 1 - p = a / (1 + a) without cancellation, a = exp(-|2 u|)
+    const float2 z2 = mul2(z, z), t = gelu_u2(z, z2);
+    const float2 a = make_float2(ex2_ftz(-fabsf(t.x)), ex2_ftz(-fabsf(t.y)));
+    const float2 d = add2(a, dup2(1.0f));
+    const float2 r = make_float2(rcp_ftz(d.x), rcp_ftz(d.y)), ra = mul2(r, a);
+    const float2 p = make_float2(t.x <= 0.0f ? r.x : ra.x, t.y <= 0.0f ? r.y : ra.y);
+    const float2 n = make_float2(t.x <= 0.0f ? ra.x : r.x, t.y <= 0.0f ? ra.y : r.y);
+    return mul2(p, fma2(mul2(z, n), fma2(z2, dup2(6.0f * kGeluK * kGeluC), dup2(2.0f * kGeluK)), dup2(1.0f)));
   }
 }
 
@@ -155,16 +176,19 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int v, int n, const fl
 }
 
 // ---------------------------------------------------------------- norm + quantise, blocks along the row
-// The row is read once and stays in registers: statistics, then normalise, activate, and each run of
-// 128 / E lanes holds a block of 128 values, finds its amax with shuffles and writes the codes. Bound by HBM
-// (3 bytes a value in and out for bf16) only if the instructions stay near ten a value, so what a row
-// costs once should be paid by few threads:
-//   * norm_quant_warp_kernel, rows of up to 640 vectors: one warp per row, VPT vectors a lane kept packed,
-//     the parameters in shared memory, one block of sixteen warps per SM (two while rows are short).
+// The row is read once from HBM: statistics, then normalise, activate, and each run of 128 / E lanes holds a
+// block of 128 values, finds its amax with shuffles and writes the codes. Bound by HBM (3 bytes a value in
+// and out for bf16) only if the instructions stay near ten a value, so what a row costs once should be
+// paid by few threads:
+//   * norm_quant_warp_kernel, rows of up to 128 vectors: one warp per row, 1, 2 or 4 vectors a lane in
+//     registers;
+//   * norm_quant_stage_kernel, rows of up to 1024 vectors: one warp per row, which a bulk copy brings to the
+//     warp's own stage in shared memory; the warp reads it there once for the statistics and once for the
+//     codes, so that few registers and twenty warps suffice. At 32760 x 5120 bf16 LayerNorm: a row in the
+//     registers of 160 threads 169 us, in those of one warp (12 warps an SM) 154 us, so: see the table;
 //   * norm_quant_row_kernel: one block per row, for longer rows and while there are too few rows to fill
 //     the SMs, where a row's latency counts.
-template <int VPT>
-constexpr int kWarpRows = VPT > 12 ? 12 : 16;  // warps of a block: 168 registers a thread for 80 of packed row
+constexpr int kWarpRows = 16;
 
 // the packed vectors are unpacked again after this, not kept unpacked in twice the registers
 template <int N>
@@ -174,7 +198,7 @@ __device__ __forceinline__ void keep_packed(uint4 (&u)[N]) {
 }
 
 template <typename T, int NORM, int EPI, int VPT>
-__global__ void __launch_bounds__(32 * kWarpRows<VPT>, VPT <= 4 ? 2 : 1)
+__global__ void __launch_bounds__(32 * kWarpRows, 2)
     norm_quant_warp_kernel(const T* __restrict__ x, const T* __restrict__ g, const T* __restrict__ beta,
                            uint8_t* __restrict__ q, float* __restrict__ scale, float* __restrict__ mean,
                            float* __restrict__ rstd, int64_t rows, int hidden, int64_t ldx, int64_t ldq, int64_t lds,
@@ -183,12 +207,12 @@ __global__ void __launch_bounds__(32 * kWarpRows<VPT>, VPT <= 4 ? 2 : 1)
   constexpr int L = kBlk / E;  // lanes of a block of values
   constexpr bool FAST = fast_math_for<T>();
   constexpr bool EXACT = NORM == GN_NORM_NONE && EPI == EPI_NONE;
-  constexpr int kGroup = VPT < 4 ? VPT : 4;  // vectors whose scales are made together
-  static_assert(VPT % kGroup == 0 && (VPT < 4 ? VPT != 3 : true), "groups of vectors");
-  extern __shared__ uint4 params[];  // [1 or 2][32 VPT] vectors: weight, bias
+  constexpr int kGroup = VPT;  // vectors whose scales are made together
+  static_assert(VPT == 1 || VPT == 2 || VPT == 4, "a power of two");
+  extern __shared__ __align__(16) uint4 params[];  // [1 or 2][32 VPT] vectors: weight, bias
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if constexpr (NORM != GN_NORM_NONE) {
-    for (int v = threadIdx.x; v < 32 * VPT; v += 32 * kWarpRows<VPT>) {
+    for (int v = threadIdx.x; v < 32 * VPT; v += 32 * kWarpRows) {
       float w[E], b[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -203,7 +227,7 @@ __global__ void __launch_bounds__(32 * kWarpRows<VPT>, VPT <= 4 ? 2 : 1)
   const float inv_n = 1.0f / (float)hidden;
   const float2 gem = dup2(NORM == GN_NORM_RMS && gemma ? 1.0f : 0.0f);
   const bool aligned = hidden % E == 0, full = hidden == 32 * VPT * E;
-  for (int64_t m = (int64_t)blockIdx.x * kWarpRows<VPT> + warp; m < rows; m += (int64_t)gridDim.x * kWarpRows<VPT>) {
+  for (int64_t m = (int64_t)blockIdx.x * kWarpRows + warp; m < rows; m += (int64_t)gridDim.x * kWarpRows) {
     const T* row = x + m * ldx;
     uint4 raw[VPT];
     if (aligned) {
@@ -295,8 +319,8 @@ __global__ void __launch_bounds__(32 * kWarpRows<VPT>, VPT <= 4 ? 2 : 1)
         am[j] = 0.0f;
 #pragma unroll
         for (int e = 0; e < H; ++e) {
-          f[j][2 * e] = EPI == EPI_NONE ? z[e].x : q_act<EPI, FAST>(z[e].x);
-          f[j][2 * e + 1] = EPI == EPI_NONE ? z[e].y : q_act<EPI, FAST>(z[e].y);
+          if constexpr (EPI != EPI_NONE) z[e] = q_act2<EPI, FAST>(z[e]);
+          f[j][2 * e] = z[e].x, f[j][2 * e + 1] = z[e].y;
           am[j] = max_nan(am[j], max_nan(fabsf(f[j][2 * e]), fabsf(f[j][2 * e + 1])));
         }
       }
@@ -310,6 +334,188 @@ __global__ void __launch_bounds__(32 * kWarpRows<VPT>, VPT <= 4 ? 2 : 1)
         const float ij = __shfl_sync(0xffffffffu, i, src), sj = EXACT ? __shfl_sync(0xffffffffu, s, src) : 0.0f;
         if (v * E < hidden) store_codes<E, EXACT>(q + m * ldq, v, hidden, f[j], sj, ij);
       }
+    }
+  }
+}
+
+constexpr int kStageWarps = 20;
+
+template <typename T, int NORM, int EPI>
+__global__ void __launch_bounds__(32 * kStageWarps, 1)
+    norm_quant_stage_kernel(const T* __restrict__ x, const T* __restrict__ g, const T* __restrict__ beta,
+                            uint8_t* __restrict__ q, float* __restrict__ scale, float* __restrict__ mean,
+                            float* __restrict__ rstd, int64_t rows, int hidden, int64_t ldx, int64_t ldq, int64_t lds,
+                            float eps, int gemma, int slot, unsigned* err) {
+  constexpr int E = Vec<T>::N, H = E / 2;
+  constexpr int L = kBlk / E;  // lanes of a block of values
+  constexpr bool FAST = fast_math_for<T>();
+  constexpr bool EXACT = NORM == GN_NORM_NONE && EPI == EPI_NONE;
+  constexpr int kParams = NORM == GN_NORM_LN ? 2 : NORM == GN_NORM_RMS ? 1 : 0;
+  // the parameters, `slot` vectors each, then a row per warp
+  extern __shared__ __align__(16) uint4 smem_rows[];
+  __shared__ uint64_t bars[kStageWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (int)(blockDim.x >> 5);
+  uint4* params = smem_rows;
+  uint4* stage = smem_rows + slot * (kParams + warp);
+  uint64_t* bar = &bars[warp];
+  const int nfull = hidden / E, nvec = (hidden + E - 1) / E;
+  const int kfull = nfull / 32;  // rounds of 32 vectors in which every lane has a whole one
+  const uint32_t bulk = (uint32_t)nfull * 16u;
+  const int64_t step = (int64_t)gridDim.x * warps;
+  const int64_t first = (int64_t)blockIdx.x * warps + warp;
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    mbar_fence_init();
+    if (first < rows) {
+      mbar_expect_tx(bar, bulk);
+      bulk_g2s(stage, x + first * ldx, bulk, bar);
+    }
+  }
+  if constexpr (kParams > 0) {
+    for (int v = threadIdx.x; v < slot; v += (int)blockDim.x) {
+      float w[E], b[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        w[e] = v * E + e < hidden ? ld_param(g, v * E + e, 1.0f) : 0.0f;
+        b[e] = NORM == GN_NORM_LN && v * E + e < hidden ? ld_param(beta, v * E + e, 0.0f) : 0.0f;
+      }
+      params[v] = Vec<T>::pack(w);
+      if (NORM == GN_NORM_LN) params[slot + v] = Vec<T>::pack(b);
+    }
+  }
+  __syncthreads();
+  const float inv_n = 1.0f / (float)hidden;
+  const float2 gem = dup2(NORM == GN_NORM_RMS && gemma ? 1.0f : 0.0f);
+  uint32_t ph = 0;
+  for (int64_t m = first; m < rows; m += step) {
+    if (!__all_sync(0xffffffffu, mbar_wait(bar, ph, err))) {
+      (void)mbar_wait(bar, ph, err);  // the copy gets a second limit to land before the warp leaves
+      return;
+    }
+    ph ^= 1u;
+    if (nvec > nfull) {  // the last vector is not whole: copied by value, zeros behind the row
+      if (lane == (nfull & 31)) stage[nfull] = load_raw<T>(x + m * ldx, nfull, hidden);
+      __syncwarp();
+    }
+    float mu = 0.0f, r = 1.0f;
+    if constexpr (NORM == GN_NORM_RMS) {
+      float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+      for (int v = lane; v < nvec; v += 32) {
+        float2 f[H];
+        unpack2<T>(stage[v], f);
+#pragma unroll
+        for (int e = 0; e < H; ++e) acc = fma2(f[e], f[e], acc);
+      }
+      r = rsqrtf(fmaf(group_sum<32>(acc.x + acc.y), inv_n, eps));
+    }
+    if constexpr (NORM == GN_NORM_LN) {
+      // sums of x - K and (x - K)^2 for a K near the mean (that of the row's first 32 vectors): mean
+      // = K + d, var = mean((x - K)^2) - d^2, which loses at most three bits while d^2 <= 4 var; a row whose
+      // beginning is further off than that gets a second pass around its mean
+      auto sums = [&](float k, float2& s1, float2& s2) {
+        s1 = s2 = make_float2(0.0f, 0.0f);
+        const float2 nk = dup2(-k);
+#pragma unroll 4
+        for (int j = 0; j < kfull; ++j) {
+          float2 f[H];
+          unpack2<T>(stage[lane + 32 * j], f);
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            const float2 d = add2(f[e], nk);
+            s1 = add2(s1, d);
+            s2 = fma2(d, d, s2);
+          }
+        }
+        const int v = lane + 32 * kfull;
+        if (v < nvec) {
+          float2 f[H];
+          unpack2<T>(stage[v], f);
+          const int left = hidden - v * E;
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            const float2 t = add2(f[e], nk);
+            const float2 d = make_float2(2 * e < left ? t.x : 0.0f, 2 * e + 1 < left ? t.y : 0.0f);
+            s1 = add2(s1, d);
+            s2 = fma2(d, d, s2);
+          }
+        }
+      };
+      float2 f[H], t = make_float2(0.0f, 0.0f);  // (nvec > 128: the first 32 vectors are whole)
+      unpack2<T>(stage[lane], f);
+#pragma unroll
+      for (int e = 0; e < H; ++e) t = add2(t, f[e]);
+      float k = group_sum<32>(t.x + t.y) * (1.0f / (32 * E));
+      float2 s1, s2;
+      sums(k, s1, s2);
+      float d = group_sum<32>(s1.x + s1.y) * inv_n;
+      float var = fmaf(-d, d, group_sum<32>(s2.x + s2.y) * inv_n);
+      if (!(d * d <= 4.0f * var)) {  // uniform over the warp
+        k += d;
+        sums(k, s1, s2);
+        d = group_sum<32>(s1.x + s1.y) * inv_n;
+        var = fmaf(-d, d, group_sum<32>(s2.x + s2.y) * inv_n);
+      }
+      mu = k + d;
+      r = rsqrtf((var < 0.0f ? 0.0f : var) + eps);
+    }
+    if constexpr (NORM != GN_NORM_NONE) {
+      if (lane == 0) {
+        if (mean && NORM == GN_NORM_LN) mean[m] = mu;
+        if (rstd) rstd[m] = r;
+      }
+    }
+    uint8_t* qrow = q + m * ldq;
+    auto four = [&](int k0, auto checked) {  // vectors lane + 32 (k0 .. k0 + 3)
+      constexpr bool CHECK = decltype(checked)::value;
+      float f[4][E], am[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int v = lane + 32 * (k0 + j);
+        am[j] = 0.0f;
+        if (CHECK && v >= nvec) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) f[j][e] = 0.0f;
+          continue;
+        }
+        float2 z[H];
+        unpack2<T>(stage[v], z);
+        if constexpr (NORM != GN_NORM_NONE) {
+          float2 w[H], b[H];
+          unpack2<T>(params[v], w);
+          if constexpr (NORM == GN_NORM_LN) unpack2<T>(params[slot + v], b);
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            if constexpr (NORM == GN_NORM_LN) z[e] = fma2(mul2(add2(z[e], dup2(-mu)), dup2(r)), w[e], b[e]);
+            else z[e] = mul2(mul2(z[e], dup2(r)), add2(w[e], gem));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          if constexpr (EPI != EPI_NONE) z[e] = q_act2<EPI, FAST>(z[e]);
+          f[j][2 * e] = z[e].x, f[j][2 * e + 1] = z[e].y;
+          am[j] = max_nan(am[j], max_nan(fabsf(z[e].x), fabsf(z[e].y)));
+        }
+      }
+      // each lane makes the scale of one of its group's four blocks
+      const float s = block_scale(group_max<4, L>(am, lane)), i = inverse<EXACT>(s);
+      const int vs = lane + 32 * (k0 + value_of_lane<4, L>(lane));
+      if (lane % (L / 4) == 0 && (!CHECK || vs / L * kBlk < hidden)) scale[m * lds + vs / L] = s;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int v = lane + 32 * (k0 + j), src = lane_of_value<4, L>(lane, j);
+        const float ij = __shfl_sync(0xffffffffu, i, src), sj = EXACT ? __shfl_sync(0xffffffffu, s, src) : 0.0f;
+        if (!CHECK || v < nvec) store_codes<E, EXACT>(qrow, v, CHECK ? hidden : INT32_MAX, f[j], sj, ij);
+      }
+    };
+    int k0 = 0;
+    for (; k0 + 4 <= kfull; k0 += 4) four(k0, std::false_type{});
+    if (32 * k0 < nvec) four(k0, std::true_type{});
+    __syncwarp();  // every lane has read the row: the next one may take its place
+    if (lane == 0 && m + step < rows) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_expect_tx(bar, bulk);
+      bulk_g2s(stage, x + (m + step) * ldx, bulk, bar);
     }
   }
 }
@@ -425,9 +631,12 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_quant_row_kernel(c
   for (int k = 0; k < VPT; ++k) {
     am[k] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if constexpr (EPI != EPI_NONE) f[k][e] = q_act<EPI, FAST>(f[k][e]);
-      am[k] = max_nan(am[k], fabsf(f[k][e]));
+    for (int e = 0; e < E; e += 2) {
+      if constexpr (EPI != EPI_NONE) {
+        const float2 z = q_act2<EPI, FAST>(make_float2(f[k][e], f[k][e + 1]));
+        f[k][e] = z.x, f[k][e + 1] = z.y;
+      }
+      am[k] = max_nan(am[k], max_nan(fabsf(f[k][e]), fabsf(f[k][e + 1])));
     }
   }
   // each lane makes the scale of one of its group's VPT blocks
@@ -509,7 +718,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
       float d[E];
       Vec<T>::unpack(rawd[i], d);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[i][e] = d[e] * q_grad<EPI, FAST>(f[i][e]);
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = mul2(make_float2(d[e], d[e + 1]), q_grad2<EPI, FAST>(make_float2(f[i][e], f[i][e + 1])));
+        f[i][e] = v.x, f[i][e + 1] = v.y;
+      }
     }
   }
   float cmax[E], csum[E];
@@ -676,17 +888,15 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
 
 // ---------------------------------------------------------------- host side
 
-// shape > 0: one warp per row with that many vectors a lane; -1, -4: one block per row with 1 or 4 vectors
-// a thread
+// shape 1, 2, 4: one warp per row with that many vectors a lane; 0: staged rows; -1, -4: one block per row with
+// 1 or 4 vectors a thread
 template <typename T, int NORM, int EPI>
 void* pick_norm_shape(int shape) {
   switch (shape) {
     case 1: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 1>;
     case 2: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 2>;
     case 4: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 4>;
-    case 8: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 8>;
-    case 12: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 12>;
-    case 20: return (void*)norm_quant_warp_kernel<T, NORM, EPI, 20>;
+    case 0: return (void*)norm_quant_stage_kernel<T, NORM, EPI>;
     case -1: return (void*)norm_quant_row_kernel<T, NORM, EPI, 1>;
     default: return (void*)norm_quant_row_kernel<T, NORM, EPI, 4>;
   }
@@ -736,16 +946,32 @@ extern "C" gn_status gn_norm_quant_fp8(const void* x, const void* g, const void*
   const int lanes = (nvec + 31) / 32;  // vectors a lane of a warp would hold
   const int sms = sm_count() > 0 ? sm_count() : 148;
   int h = (int)hidden;
-  if (lanes <= 20 && (lanes == 1 || rows > 4 * sms)) {
-    const int shape = lanes <= 2 ? lanes : lanes <= 4 ? 4 : lanes <= 8 ? 8 : lanes <= 12 ? 12 : 20;
+  const int vectors = norm == GN_NORM_LN ? 2 : norm == GN_NORM_RMS ? 1 : 0;  // parameters
+  if (lanes <= 4 && (lanes == 1 || rows > 4 * sms)) {
+    const int shape = lanes <= 2 ? lanes : 4;
     void* kern = dt == GN_BF16 ? pick_norm<__nv_bfloat16>(norm, epi, shape) : pick_norm<float>(norm, epi, shape);
-    const size_t smem = norm == GN_NORM_NONE ? 0 : (size_t)(norm == GN_NORM_LN ? 2 : 1) * 32 * shape * 16;
-    const int warps = shape == 20 ? kWarpRows<20> : kWarpRows<1>;
-    const int most = persistent_grid(kern, 32 * warps, smem, 0);
+    const size_t smem = (size_t)vectors * 32 * shape * 16;
+    const int most = persistent_grid(kern, 32 * kWarpRows, smem, 0);
     if (most <= 0) return GN_ERR_CUDA;
-    const int64_t blocks = (rows + warps - 1) / warps;
+    const int64_t blocks = (rows + kWarpRows - 1) / kWarpRows;
     void* args[] = {&x, &g, &beta, &q, &scale, &mean, &rstd, &rows, &h, &ld_x, &ld_q, &ld_s, &eps, &gemma};
-    if (cudaLaunchKernel(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3((unsigned)(32 * warps)), args, smem,
+    if (cudaLaunchKernel(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(32 * kWarpRows), args, smem,
+                         (cudaStream_t)stream) != cudaSuccess)
+      return GN_ERR_CUDA;
+  } else if (nvec > 128 && nvec <= 1024 && rows > 4 * sms) {
+    void* kern = dt == GN_BF16 ? pick_norm<__nv_bfloat16>(norm, epi, 0) : pick_norm<float>(norm, epi, 0);
+    int slot = (nvec + 7) / 8 * 8;
+    const size_t room = smem_optin() > 1024 ? smem_optin() - 1024 : 0;  // the barriers are static
+    int warps = (int)(room / ((size_t)slot * 16)) - vectors;
+    if (warps > kStageWarps) warps = kStageWarps;
+    if (warps < 1) return GN_ERR_UNSUPPORTED;
+    const size_t smem = (size_t)(vectors + warps) * slot * 16;
+    if (!kernel_attrs(kern, smem)) return GN_ERR_CUDA;
+    unsigned* err = device_err_word();
+    if (!err) return GN_ERR_CUDA;
+    const int64_t blocks = (rows + warps - 1) / warps;
+    void* args[] = {&x, &g, &beta, &q, &scale, &mean, &rstd, &rows, &h, &ld_x, &ld_q, &ld_s, &eps, &gemma, &slot, &err};
+    if (cudaLaunchKernel(kern, dim3((unsigned)(blocks < sms ? blocks : sms)), dim3((unsigned)(32 * warps)), args, smem,
                          (cudaStream_t)stream) != cudaSuccess)
       return GN_ERR_CUDA;
   } else {
