@@ -97,7 +97,8 @@ def check(t, G, dt, act, eps=1e-5, w=True, b=True, shape=None):
 # (N, S, C, G): one position; one value a group (variance 0); groups that cross 16-byte vectors; one
 # group; as many groups as channels; widths that end inside a vector; many small images; long images
 SHAPES = [(1, 1, 64, 8), (2, 1, 8, 8), (1, 63, 320, 32), (3, 17, 30, 3), (2, 50, 40, 1), (2, 33, 24, 24), (2, 65, 77, 7),
-          (33, 5, 64, 4), (1, 4099, 128, 32), (2, 1031, 640, 32), (1, 300, 1536, 16), (1, 20000, 64, 32)]
+          (33, 5, 64, 4), (1, 4099, 128, 32), (2, 1031, 640, 32), (1, 300, 1536, 16), (1, 20000, 64, 32), (2, 4096, 640, 32), (1, 70000, 64, 4), (2, 30001, 48, 3), (1, 9000, 520, 1),
+          (1, 17, 8192, 2), (1, 40, 4104, 27), (300, 7, 32, 2)]
 
 
 @pytest.mark.gpu
@@ -265,12 +266,16 @@ def bwd(x=P, mean=P, rstd=P, dy=P, dx=P, ws=P, nws=1 << 40, N=2, S=10, C=64, G=4
     return gn.gn_groupnorm_bwd(x, None, None, mean, rstd, dy, dx, None, None, ws, nws, N, S, C, G, ldx, lddy, lddx, epi, dt, None)
 
 
+# an image that is not kept on chip: the forward needs its workspace
+BIG = dict(S=100000, C=512, G=32, ldx=512, ldy=512)
+
+
 @pytest.mark.parametrize("call,kw,status", [
     (fwd, dict(dt=3), gn.GN_ERR_DTYPE), (fwd, dict(epi=7), gn.GN_ERR_DTYPE), (fwd, dict(G=5), gn.GN_ERR_SHAPE),
     (fwd, dict(G=0), gn.GN_ERR_SHAPE), (fwd, dict(C=0), gn.GN_ERR_SHAPE), (fwd, dict(N=-1), gn.GN_ERR_SHAPE),
     (fwd, dict(ldx=63), gn.GN_ERR_SHAPE), (fwd, dict(ldy=32), gn.GN_ERR_SHAPE), (fwd, dict(x=None), gn.GN_ERR_NULL),
     (fwd, dict(y=None), gn.GN_ERR_NULL), (fwd, dict(x=P + 8), gn.GN_ERR_ALIGN), (fwd, dict(ldx=65), gn.GN_ERR_ALIGN),
-    (fwd, dict(ws=None), gn.GN_ERR_WORKSPACE), (fwd, dict(nws=8), gn.GN_ERR_WORKSPACE), (fwd, dict(ws=P + 4), gn.GN_ERR_ALIGN),
+    (fwd, dict(BIG, ws=None), gn.GN_ERR_WORKSPACE), (fwd, dict(BIG, nws=8), gn.GN_ERR_WORKSPACE), (fwd, dict(BIG, ws=P + 4), gn.GN_ERR_ALIGN),
     (fwd, dict(N=0, x=None, ws=None), gn.GN_OK), (fwd, dict(S=0, x=None, ws=None), gn.GN_OK),
     (bwd, dict(mean=None), gn.GN_ERR_NULL), (bwd, dict(rstd=None), gn.GN_ERR_NULL), (bwd, dict(dy=None), gn.GN_ERR_NULL),
     (bwd, dict(lddx=60), gn.GN_ERR_SHAPE), (bwd, dict(lddy=68), gn.GN_ERR_ALIGN), (bwd, dict(nws=0), gn.GN_ERR_WORKSPACE),

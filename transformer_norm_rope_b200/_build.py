@@ -45,7 +45,7 @@ def _deps():
 # the tensor-core products live in other files
 STEP_SOURCES = ("api.cu", "rmsnorm.cu", "layernorm.cu", "norm_fwd_warp.cu", "rope.cu")
 # headers that none of them includes
-TENSOR_CORE_HEADERS = ("tcgen05.cuh",)
+OTHER_HEADERS = ("tcgen05.cuh", "act_pairs.cuh")
 
 
 def sources_digest(step_only: bool = False) -> str:
@@ -55,7 +55,7 @@ def sources_digest(step_only: bool = False) -> str:
 
     srcs = [p for p in sources() if not step_only or os.path.basename(p) in STEP_SOURCES]
     hdrs = [p for p in glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-            if not step_only or os.path.basename(p) not in TENSOR_CORE_HEADERS]
+            if not step_only or os.path.basename(p) not in OTHER_HEADERS]
     h = hashlib.sha256()
     for p in sorted(srcs + hdrs):
         h.update(os.path.basename(p).encode())

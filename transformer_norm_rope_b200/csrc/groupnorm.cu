@@ -10,12 +10,14 @@
 // Unlike the row norms a group's values are not contiguous: a position's group is a run of P channels,
 // P * sizeof(T) bytes (20 to 128 in practice), and positions lie C channels apart.
 //
-// Two passes over the image: a pass over slabs of positions that reduces every channel of the slab
+// Images whose groups fit on chip are read once (the resident kernels, further down). Longer ones take
+// two passes: a pass over slabs of positions that reduces every channel of the slab
 // (gn_stats_kernel, gn_bwd_sums_kernel), a small kernel that joins the slabs and the channels of a
 // group in a fixed order, and an elementwise pass. A thread keeps one 16-byte vector of channels and
 // walks down the positions, so its per-channel sums and parameters stay in registers and every warp
 // access covers whole runs of a row. The forward's sums are (mean, centred sum of squares) per
 // channel, batch by batch with Chan's update: no E[x^2] - E[x]^2 cancellation.
+#include "act_pairs.cuh"
 #include "gn_common.cuh"
 #include "gn_host.h"
 
@@ -222,7 +224,10 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(const T* x, int64_t 
     float f[E];
     load_vec<T>(x + (img + r) * ldx, p.v, g.C, p.whole, f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = epi_fwd<EPI, FAST>(fmaf(f[e] - mu[e], a[e], sh[e]));
+    for (int e = 0; e < E; e += 2) {
+      const float2 z = act_pair<EPI, FAST>(make_float2(fmaf(f[e] - mu[e], a[e], sh[e]), fmaf(f[e + 1] - mu[e + 1], a[e + 1], sh[e + 1])));
+      f[e] = z.x, f[e + 1] = z.y;
+    }
     store_vec<T>(y + (img + r) * ldy, p.v, g.C, p.whole, f);
   }
 }
@@ -261,11 +266,12 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const T* __restri
       load_vec<T>(x + (img + r) * ldx, p.v, g.C, p.whole, f);
       load_vec<T>(dy + (img + r) * lddy, p.v, g.C, p.whole, d);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float xh = (f[e] - mu[e]) * s[e];
-        const float gg = d[e] * epi_grad<EPI, FAST>(fmaf(xh, wf[e], bf[e]));
-        A[e] += gg;
-        B[e] = fmaf(gg, xh, B[e]);
+      for (int e = 0; e < E; e += 2) {
+        const float2 xh = make_float2((f[e] - mu[e]) * s[e], (f[e + 1] - mu[e + 1]) * s[e + 1]);
+        const float2 gr = act_grad_pair<EPI, FAST>(make_float2(fmaf(xh.x, wf[e], bf[e]), fmaf(xh.y, wf[e + 1], bf[e + 1])));
+        const float g0 = d[e] * gr.x, g1 = d[e + 1] * gr.y;
+        A[e] += g0, A[e + 1] += g1;
+        B[e] = fmaf(g0, xh.x, B[e]), B[e + 1] = fmaf(g1, xh.y, B[e + 1]);
       }
     }
   }
@@ -343,13 +349,389 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_apply_kernel(const T* __restr
     load_vec<T>(x + (img + r) * ldx, p.v, g.C, p.whole, f);
     load_vec<T>(dy + (img + r) * lddy, p.v, g.C, p.whole, d);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float xh = (f[e] - mu[e]) * s[e];
-      const float gg = d[e] * epi_grad<EPI, FAST>(fmaf(xh, wf[e], bf[e]));
-      f[e] = s[e] * (fmaf(gg, wf[e], -m1[e]) - xh * m2[e]);
+    for (int e = 0; e < E; e += 2) {
+      const float2 xh = make_float2((f[e] - mu[e]) * s[e], (f[e + 1] - mu[e + 1]) * s[e + 1]);
+      const float2 gr = act_grad_pair<EPI, FAST>(make_float2(fmaf(xh.x, wf[e], bf[e]), fmaf(xh.y, wf[e + 1], bf[e + 1])));
+      f[e] = s[e] * (fmaf(d[e] * gr.x, wf[e], -m1[e]) - xh.x * m2[e]);
+      f[e + 1] = s[e + 1] * (fmaf(d[e + 1] * gr.y, wf[e + 1], -m1[e + 1]) - xh.y * m2[e + 1]);
     }
     store_vec<T>(dx + (img + r) * lddx, p.v, g.C, p.whole, f);
   }
+}
+
+// ---------------------------------------------------------------- resident images: one read
+// When the runs of a few whole groups over an image fit the registers of a cluster of at most eight blocks,
+// the cluster loads them once: block r the positions [r S / cs, (r + 1) S / cs), a thread one 16-byte
+// vector of the run at every RL-th position, VPT in all, kept packed. Sums go channel by channel through
+// shared memory, then across the cluster through distributed shared memory, in a fixed order. One launch,
+// 2 n (forward) or 3 n (backward) values of traffic; runs are at least 64 bytes where the groups allow
+// it, so that sectors are used whole.
+constexpr int kResThreads = 512;
+
+struct Bundle {
+  int64_t S;
+  int C, P, G;
+  int groups;   // groups of a bundle
+  int bv;       // its 16-byte vectors
+  int bundles;  // of an image
+  int cs;       // blocks of a cluster
+};
+
+template <int N>
+__device__ __forceinline__ void keep_packed(uint4 (&u)[N]) {  // unpack again after this; do not keep unpacked
+#pragma unroll
+  for (int k = 0; k < N; ++k) asm volatile("" : "+r"(u[k].x), "+r"(u[k].y), "+r"(u[k].z), "+r"(u[k].w));
+}
+
+__device__ __forceinline__ uint32_t cluster_rank_() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float2 peer_f2(const float2* p, int rank) {  // the same place in block `rank`
+  uint32_t a;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// what a thread of the resident kernels works on
+template <int E>
+struct ResPlace {
+  int n, c0, nch, lv, lr, rl, rank;
+  bool active;
+  int64_t r0, r1;
+  __device__ __forceinline__ ResPlace(const Bundle& g) {
+    rank = (int)cluster_rank_();
+    const int unit = blockIdx.x / g.cs;
+    n = unit / g.bundles;
+    c0 = (unit % g.bundles) * g.groups * g.P;
+    nch = g.C - c0 < g.groups * g.P ? g.C - c0 : g.groups * g.P;
+    rl = kResThreads / g.bv;
+    lr = threadIdx.x / g.bv;
+    lv = threadIdx.x % g.bv;
+    active = lr < rl && lv * E < nch;
+    r0 = g.S * rank / g.cs;
+    r1 = g.S * (rank + 1) / g.cs;
+  }
+};
+
+template <typename T, int VPT>
+__device__ __forceinline__ void res_load(uint4 (&raw)[VPT], const T* x, int64_t ld, const ResPlace<Vec<T>::N>& p,
+                                         int64_t S) {
+  const T* base = x + ((int64_t)p.n * S + p.r0 + p.lr) * ld + p.c0 + p.lv * Vec<T>::N;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    raw[k] = make_uint4(0, 0, 0, 0);
+    if (p.active && p.r0 + p.lr + (int64_t)k * p.rl < p.r1) raw[k] = ld_stream(base + (int64_t)k * p.rl * ld);
+  }
+}
+
+// Sums over the block's positions of NQ quantities per channel. v: this thread's E channels (0 where it is not
+// active). red: NQ x kResThreads x E floats. Returns the part sums in red2[q][part][W] (W = bv E, `parts`
+// parts), after a barrier; red and red2 may be the same memory (a barrier lies between).
+template <int E, int NQ>
+__device__ __forceinline__ int res_parts(const float (&v)[NQ][E], float* red, int W, int rl, bool in) {
+  const int tid = threadIdx.x;
+  if (in) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<float4*>(red + q * kResThreads * E + tid * E + e) =
+            make_float4(v[q][e], v[q][e + 1], v[q][e + 2], v[q][e + 3]);
+  }
+  __syncthreads();
+  const int parts = W < kResThreads ? kResThreads / W < rl ? kResThreads / W : rl : 1;
+  // thread (part, channel) adds every parts-th position; blocks wider than kResThreads channels in rounds
+  for (int c0 = 0; c0 < W; c0 += kResThreads) {
+    const int c = c0 + (W < kResThreads ? tid % W : tid), part = W < kResThreads ? tid / W : 0;
+    float t[NQ];
+    const bool mine = part < parts && c < W;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) t[q] = 0.0f;
+    if (mine)
+      for (int r = part; r < rl; r += parts)
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) t[q] += red[q * kResThreads * E + r * W + c];
+    __syncthreads();
+    if (mine)  // the place of a position that this thread has read (rows below `parts` of its own channels)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) red[q * kResThreads * E + part * W + c] = t[q];
+  }
+  __syncthreads();
+  return parts;
+}
+
+__device__ __forceinline__ float warp_sum_of(const float* red, int W, int parts, int ch0, int P, int lane) {
+  float t = 0.0f;
+  for (int i = lane; i < P * parts; i += 32) t += red[(i / P) * W + ch0 + i % P];
+  return group_sum<32>(t);
+}
+
+template <typename T, int EPI, int VPT>
+__global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
+    gn_fwd_resident_kernel(const T* x, int64_t ldx, const T* __restrict__ w, const T* __restrict__ b, Bundle g, float eps,
+                           T* y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd) {
+  constexpr int E = Vec<T>::N, H = E / 2;
+  constexpr bool FAST = fast_math_for<T>();
+  extern __shared__ __align__(16) float smem[];
+  const int W = g.bv * E;
+  float* red = smem;                                        // [kResThreads][E]
+  float2* own = reinterpret_cast<float2*>(red + kResThreads * E);  // [groups] (mean, centred squares) of the block
+  float2* stat = own + g.groups;                            // [groups] (mean, rstd) of the image
+  float* chan = reinterpret_cast<float*>(stat + g.groups);  // [3][W] mean, scale, shift of a channel
+  const ResPlace<E> p(g);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ng = p.nch / g.P;
+  uint4 raw[VPT];
+  res_load<T, VPT>(raw, x, ldx, p, g.S);
+  const float cnt = (float)((p.r1 - p.r0) * g.P), inv_cnt = cnt > 0.0f ? 1.0f / cnt : 0.0f;
+  {
+    float s[1][E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[0][e] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      float f[E];
+      Vec<T>::unpack(raw[k], f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[0][e] += f[e];
+    }
+    const int parts = res_parts<E, 1>(s, red, W, p.rl, p.lr < p.rl);
+    for (int i = warp; i < ng; i += kResThreads / 32) {
+      const float t = warp_sum_of(red, W, parts, i * g.P, g.P, lane);
+      if (lane == 0) own[i].x = t * inv_cnt;
+    }
+    __syncthreads();
+    keep_packed(raw);
+    float mu[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      s[0][e] = 0.0f;
+      mu[e] = p.active ? own[(p.lv * E + e) / g.P].x : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      if (p.r0 + p.lr + (int64_t)k * p.rl < p.r1) {
+        float f[E];
+        Vec<T>::unpack(raw[k], f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[0][e] = fmaf(f[e] - mu[e], f[e] - mu[e], s[0][e]);
+      }
+    }
+    const int parts2 = res_parts<E, 1>(s, red, W, p.rl, p.lr < p.rl);
+    for (int i = warp; i < ng; i += kResThreads / 32) {
+      const float t = warp_sum_of(red, W, parts2, i * g.P, g.P, lane);
+      if (lane == 0) own[i].y = t;
+    }
+    keep_packed(raw);
+  }
+  if (g.cs > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < ng; i += kResThreads) {
+    const float total = (float)((double)g.S * g.P);
+    float mu, q = 0.0f;
+    if (g.cs > 1) {  // join the blocks' statistics in rank order
+      float t = 0.0f;
+      for (int r = 0; r < g.cs; ++r)
+        t = fmaf((float)((g.S * (r + 1) / g.cs - g.S * r / g.cs) * g.P), peer_f2(own + i, r).x, t);
+      mu = t / total;
+      for (int r = 0; r < g.cs; ++r) {
+        const float2 v = peer_f2(own + i, r);
+        const float d = v.x - mu;
+        q += fmaf((float)((g.S * (r + 1) / g.cs - g.S * r / g.cs) * g.P) * d, d, v.y);
+      }
+    } else {
+      mu = own[i].x;
+      q = own[i].y;
+    }
+    const float s = 1.0f / sqrtf(q / total + eps);
+    stat[i] = make_float2(mu, s);
+    if (p.rank == 0) {
+      const int64_t at = (int64_t)p.n * g.G + p.c0 / g.P + i;
+      if (mean) mean[at] = mu;
+      if (rstd) rstd[at] = s;
+    }
+  }
+  if (g.cs > 1) cluster_arrive();  // this block has read its peers (they may leave once all have)
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.nch; c += kResThreads) {
+    const float2 s = stat[c / g.P];
+    chan[c] = s.x;
+    chan[W + c] = s.y * ld_param(w, p.c0 + c, 1.0f);
+    chan[2 * W + c] = ld_param(b, p.c0 + c, 0.0f);
+  }
+  __syncthreads();
+  if (p.active) {
+    float2 mu[H], a[H], sh[H];
+#pragma unroll
+    for (int e = 0; e < H; ++e) {
+      const int c = p.lv * E + 2 * e;
+      mu[e] = make_float2(-chan[c], -chan[c + 1]);
+      a[e] = make_float2(chan[W + c], chan[W + c + 1]);
+      sh[e] = make_float2(chan[2 * W + c], chan[2 * W + c + 1]);
+    }
+    T* out = y + ((int64_t)p.n * g.S + p.r0 + p.lr) * ldy + p.c0 + p.lv * E;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      if (p.r0 + p.lr + (int64_t)k * p.rl >= p.r1) break;
+      float2 f[H];
+      unpack2<T>(raw[k], f);
+#pragma unroll
+      for (int e = 0; e < H; ++e) f[e] = act_pair<EPI, FAST>(fma2(add2(f[e], mu[e]), a[e], sh[e]));
+      st_stream(out + (int64_t)k * p.rl * ldy, pack2<T>(f));
+    }
+  }
+  if (g.cs > 1) cluster_wait();
+}
+
+// chan_out[n][0..C) = B_c, [C..2C) = A_c of the image
+template <typename T, int EPI, int VPT>
+__global__ void __launch_bounds__(kResThreads, VPT <= 2 ? 2 : 1)
+    gn_bwd_resident_kernel(const T* __restrict__ x, int64_t ldx, const T* dy, int64_t lddy, const T* __restrict__ w,
+                           const T* __restrict__ b, const float* __restrict__ mean, const float* __restrict__ rstd,
+                           Bundle g, T* dx, int64_t lddx, float* __restrict__ chan_out) {
+  constexpr int E = Vec<T>::N, H = E / 2;
+  constexpr bool FAST = fast_math_for<T>();
+  extern __shared__ __align__(16) float smem[];
+  const int W = g.bv * E;
+  float* red = smem;                                                   // [2][kResThreads][E]
+  float2* own = reinterpret_cast<float2*>(red + 2 * kResThreads * E);  // [W] (A_c, B_c) of the block
+  float2* tot = own + W;                                               // [W] of the image, times w_c
+  float2* stat = tot + W;                                              // [groups] (m1, m2)
+  float* chan = reinterpret_cast<float*>(stat + g.groups);             // [4][W] mean, rstd, w, b of a channel
+  const ResPlace<E> p(g);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ng = p.nch / g.P;
+  uint4 raw[VPT], rawd[VPT];
+  res_load<T, VPT>(raw, x, ldx, p, g.S);
+  res_load<T, VPT>(rawd, dy, lddy, p, g.S);
+  for (int c = threadIdx.x; c < p.nch; c += kResThreads) {
+    const int64_t at = (int64_t)p.n * g.G + (p.c0 + c) / g.P;
+    chan[c] = mean[at];
+    chan[W + c] = rstd[at];
+    chan[2 * W + c] = ld_param(w, p.c0 + c, 1.0f);
+    chan[3 * W + c] = ld_param(b, p.c0 + c, 0.0f);
+  }
+  __syncthreads();
+  float2 mu[H], s[H], wf[H], bf[H];
+#pragma unroll
+  for (int e = 0; e < H; ++e) {
+    const int c = p.active ? p.lv * E + 2 * e : 0;
+    mu[e] = make_float2(-chan[c], -chan[c + 1]);
+    s[e] = make_float2(chan[W + c], chan[W + c + 1]);
+    wf[e] = make_float2(chan[2 * W + c], chan[2 * W + c + 1]);
+    bf[e] = make_float2(chan[3 * W + c], chan[3 * W + c + 1]);
+  }
+  float v[2][E];
+  {
+    float2 A[H], B[H];
+#pragma unroll
+    for (int e = 0; e < H; ++e) A[e] = B[e] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      if (p.r0 + p.lr + (int64_t)k * p.rl >= p.r1) break;
+      float2 f[H], d[H];
+      unpack2<T>(raw[k], f);
+      unpack2<T>(rawd[k], d);
+#pragma unroll
+      for (int e = 0; e < H; ++e) {
+        const float2 xh = mul2(add2(f[e], mu[e]), s[e]);
+        const float2 gg = EPI == EPI_NONE ? d[e] : mul2(d[e], act_grad_pair<EPI, FAST>(fma2(xh, wf[e], bf[e])));
+        A[e] = add2(A[e], gg);
+        B[e] = fma2(gg, xh, B[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < H; ++e) {
+      v[0][2 * e] = p.active ? A[e].x : 0.0f, v[0][2 * e + 1] = p.active ? A[e].y : 0.0f;
+      v[1][2 * e] = p.active ? B[e].x : 0.0f, v[1][2 * e + 1] = p.active ? B[e].y : 0.0f;
+    }
+  }
+  keep_packed(raw);
+  keep_packed(rawd);
+  const int parts = res_parts<E, 2>(v, red, W, p.rl, p.lr < p.rl);
+  for (int c = threadIdx.x; c < p.nch; c += kResThreads) {
+    float ta = 0.0f, tb = 0.0f;
+    for (int k = 0; k < parts; ++k) {
+      ta += red[k * W + c];
+      tb += red[kResThreads * E + k * W + c];
+    }
+    own[c] = make_float2(ta, tb);
+  }
+  if (g.cs > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  for (int c = threadIdx.x; c < p.nch; c += kResThreads) {
+    float2 t = make_float2(0.0f, 0.0f);
+    if (g.cs > 1) {
+      for (int r = 0; r < g.cs; ++r) t = add2(t, peer_f2(own + c, r));
+    } else {
+      t = own[c];
+    }
+    if (chan_out && p.rank == 0) {
+      chan_out[(int64_t)p.n * 2 * g.C + p.c0 + c] = t.y;
+      chan_out[(int64_t)p.n * 2 * g.C + g.C + p.c0 + c] = t.x;
+    }
+    tot[c] = mul2(t, dup2(chan[2 * W + c]));
+  }
+  if (g.cs > 1) cluster_arrive();  // this block has read its peers (they may leave once all have)
+  __syncthreads();
+  const float inv = 1.0f / (float)((double)g.S * g.P);
+  for (int i = warp; i < ng; i += kResThreads / 32) {
+    float m1 = 0.0f, m2 = 0.0f;
+    for (int c = lane; c < g.P; c += 32) {
+      const float2 t = tot[i * g.P + c];
+      m1 += t.x;
+      m2 += t.y;
+    }
+    m1 = group_sum<32>(m1) * inv;
+    m2 = group_sum<32>(m2) * inv;
+    if (lane == 0) stat[i] = make_float2(m1, m2);
+  }
+  __syncthreads();
+  if (p.active) {
+    float2 m1[H], m2[H];
+#pragma unroll
+    for (int e = 0; e < H; ++e) {
+      const float2 u = stat[(p.lv * E + 2 * e) / g.P], t = stat[(p.lv * E + 2 * e + 1) / g.P];
+      m1[e] = make_float2(-u.x, -t.x);
+      m2[e] = make_float2(-u.y, -t.y);
+    }
+    T* out = dx + ((int64_t)p.n * g.S + p.r0 + p.lr) * lddx + p.c0 + p.lv * E;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      if (p.r0 + p.lr + (int64_t)k * p.rl >= p.r1) break;
+      float2 f[H], d[H];
+      unpack2<T>(raw[k], f);
+      unpack2<T>(rawd[k], d);
+#pragma unroll
+      for (int e = 0; e < H; ++e) {
+        const float2 xh = mul2(add2(f[e], mu[e]), s[e]);
+        const float2 gg = EPI == EPI_NONE ? d[e] : mul2(d[e], act_grad_pair<EPI, FAST>(fma2(xh, wf[e], bf[e])));
+        f[e] = mul2(s[e], fma2(xh, m2[e], fma2(gg, wf[e], m1[e])));
+      }
+      st_stream(out + (int64_t)k * p.rl * lddx, pack2<T>(f));
+    }
+  }
+  if (g.cs > 1) cluster_wait();
 }
 
 // ---------------------------------------------------------------- host side
@@ -409,6 +791,93 @@ gn_status launch(void* kern, int64_t blocks, void** args, cudaStream_t s) {
   return launch_status();
 }
 
+// How the resident kernels would take the shape; cs == 0: it does not fit. most: the vectors a thread
+// may hold (of each tensor). A bundle is the fewest groups whose run is whole vectors, widened to 64 bytes
+// while that still fits; the cluster has as many blocks as it takes to fill the SMs or to hold the run.
+Bundle plan_resident(int64_t N, int64_t S, int64_t C, int64_t G, int es, int most, int* vpt) {
+  Bundle g{};
+  g.S = S;
+  g.C = (int)C;
+  g.G = (int)G;
+  g.P = (int)(C / G);
+  g.cs = 0;
+  const int64_t run = (int64_t)g.P * es;  // bytes of one group at one position
+  if (C * es % 16 || S > (1 << 20)) return g;
+  int per = 1;
+  while (per * run % 16) per *= 2;  // run * per is whole vectors for some power of two up to 16
+  if (per > G) return g;
+  int64_t bv = per * run / 16;
+  auto fits = [&](int64_t v, int64_t cs) { return v <= kResThreads && (S + cs - 1) / cs <= (kResThreads / v) * (int64_t)most; };
+  if (!fits(bv, 8)) return g;
+  while (bv < 4 && per * 2 <= G && fits(bv * 2, 8)) per *= 2, bv *= 2;
+  g.groups = per;
+  g.bv = (int)bv;
+  g.bundles = (int)((G + per - 1) / per);
+  const int sms = sm_count() > 0 ? sm_count() : 148;
+  const int64_t units = N * g.bundles;
+  int cs = 1;
+  while (cs < 8 && (!fits(bv, cs) || (units * cs < 2 * sms && (S + cs - 1) / cs > 2 * (kResThreads / bv)))) cs *= 2;
+  const int64_t need = ((S + cs - 1) / cs + kResThreads / bv - 1) / (kResThreads / bv);
+  int v = 1;
+  while (v < need) v *= 2;
+  *vpt = v;
+  g.cs = cs;
+  return g;
+}
+
+template <typename T, int EPI>
+void* pick_fwd_res(int vpt) {
+  return vpt <= 1   ? (void*)gn_fwd_resident_kernel<T, EPI, 1>
+         : vpt <= 2 ? (void*)gn_fwd_resident_kernel<T, EPI, 2>
+         : vpt <= 4 ? (void*)gn_fwd_resident_kernel<T, EPI, 4>
+         : vpt <= 8 ? (void*)gn_fwd_resident_kernel<T, EPI, 8>
+                    : (void*)gn_fwd_resident_kernel<T, EPI, 16>;
+}
+template <typename T, int EPI>
+void* pick_bwd_res(int vpt) {
+  return vpt <= 1   ? (void*)gn_bwd_resident_kernel<T, EPI, 1>
+         : vpt <= 2 ? (void*)gn_bwd_resident_kernel<T, EPI, 2>
+         : vpt <= 4 ? (void*)gn_bwd_resident_kernel<T, EPI, 4>
+                    : (void*)gn_bwd_resident_kernel<T, EPI, 8>;
+}
+template <typename T>
+void* pick_res(bool fwd, int epi, int vpt) {
+  if (fwd)
+    return epi == GN_EPI_GELU_TANH ? pick_fwd_res<T, EPI_GELU_TANH>(vpt)
+           : epi == GN_EPI_SILU    ? pick_fwd_res<T, EPI_SILU>(vpt)
+                                   : pick_fwd_res<T, EPI_NONE>(vpt);
+  return epi == GN_EPI_GELU_TANH ? pick_bwd_res<T, EPI_GELU_TANH>(vpt)
+         : epi == GN_EPI_SILU    ? pick_bwd_res<T, EPI_SILU>(vpt)
+                                 : pick_bwd_res<T, EPI_NONE>(vpt);
+}
+constexpr int kFwdMost = 16, kBwdMost = 8;  // vectors a thread may hold of each tensor: 64 registers in all
+
+size_t res_smem(const Bundle& g, int es, bool fwd) {
+  const size_t E = 16 / es, W = (size_t)g.bv * E;
+  return fwd ? (kResThreads * E + 4 * g.groups + 3 * W) * 4 : (2 * kResThreads * E + 4 * W + 2 * g.groups + 4 * W) * 4;
+}
+
+gn_status launch_resident(void* kern, const Bundle& g, int64_t N, size_t smem, void** args, cudaStream_t s) {
+  const int64_t blocks = N * g.bundles * g.cs;
+  if (blocks > INT32_MAX) return GN_ERR_SHAPE;
+  if (!kernel_attrs(kern, smem)) return GN_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kResThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)g.cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelExC(&cfg, kern, args) != cudaSuccess) return GN_ERR_CUDA;
+  count_launches(1);
+  return launch_status();
+}
+
 }  // namespace
 }  // namespace gn
 
@@ -416,6 +885,8 @@ using namespace gn;
 
 extern "C" size_t gn_groupnorm_fwd_workspace(int64_t N, int64_t S, int64_t C, int64_t G, gn_dtype dt) {
   if (!dt_ok(dt) || !shape_ok(N, S, C, G) || N == 0 || S == 0) return 0;
+  int vpt = 0;
+  if (plan_resident(N, S, C, G, (int)dt_size(dt), kFwdMost, &vpt).cs) return 0;
   const GnShape g = plan(N, S, C, G, (int)dt_size(dt));
   return up16((size_t)N * g.G * 8) + (size_t)N * g.chunks * g.C * 8;
 }
@@ -430,9 +901,16 @@ extern "C" gn_status gn_groupnorm_fwd(const void* x, const void* w, const void* 
   if (!x || !y) return GN_ERR_NULL;
   const size_t es = dt_size(dt);
   if (!aligned16(x) || !aligned16(y) || ld_x * es % 16 || ld_y * es % 16) return GN_ERR_ALIGN;
+  cudaStream_t s = (cudaStream_t)stream;
+  int vpt = 0;
+  Bundle r = plan_resident(N, S, C, G, (int)es, kFwdMost, &vpt);
+  if (r.cs) {
+    void* args[] = {&x, &ld_x, &w, &b, &r, &eps, &y, &ld_y, &mean, &rstd};
+    return launch_resident(dt == GN_BF16 ? pick_res<__nv_bfloat16>(true, epi, vpt) : pick_res<float>(true, epi, vpt), r, N,
+                           res_smem(r, (int)es, true), args, s);
+  }
   if (!ws || ws_bytes < gn_groupnorm_fwd_workspace(N, S, C, G, dt)) return GN_ERR_WORKSPACE;
   if (!aligned16(ws)) return GN_ERR_ALIGN;
-  cudaStream_t s = (cudaStream_t)stream;
   GnShape g = plan(N, S, C, G, (int)es);
   float2* stat = static_cast<float2*>(ws);
   float2* part = reinterpret_cast<float2*>(static_cast<char*>(ws) + up16((size_t)N * g.G * 8));
@@ -454,6 +932,8 @@ extern "C" gn_status gn_groupnorm_fwd(const void* x, const void* w, const void* 
 
 extern "C" size_t gn_groupnorm_bwd_workspace(int64_t N, int64_t S, int64_t C, int64_t G, gn_dtype dt) {
   if (!dt_ok(dt) || !shape_ok(N, S, C, G) || N == 0 || S == 0) return 0;
+  int vpt = 0;
+  if (plan_resident(N, S, C, G, (int)dt_size(dt), kBwdMost, &vpt).cs) return (size_t)N * C * 8;
   const GnShape g = plan(N, S, C, G, (int)dt_size(dt));
   return up16((size_t)N * g.G * 8) + (size_t)N * g.C * 8 + (size_t)N * g.chunks * g.C * 8;
 }
@@ -476,6 +956,16 @@ extern "C" gn_status gn_groupnorm_bwd(const void* x, const void* w, const void* 
     return GN_ERR_ALIGN;
   if (!ws || ws_bytes < gn_groupnorm_bwd_workspace(N, S, C, G, dt)) return GN_ERR_WORKSPACE;
   if (!aligned16(ws)) return GN_ERR_ALIGN;
+  int vpt = 0;
+  Bundle r = plan_resident(N, S, C, G, (int)es, kBwdMost, &vpt);
+  if (r.cs) {
+    float* chan = dw || db ? static_cast<float*>(ws) : nullptr;
+    void* args[] = {&x, &ld_x, &dy, &ld_dy, &w, &b, &mean, &rstd, &r, &dx, &ld_dx, &chan};
+    const gn_status st = launch_resident(dt == GN_BF16 ? pick_res<__nv_bfloat16>(false, epi, vpt) : pick_res<float>(false, epi, vpt),
+                                         r, N, res_smem(r, (int)es, false), args, s);
+    if (st != GN_OK || !chan) return st;
+    return launch_colsum(chan, N, 2 * C, C, dw, db, s);
+  }
   GnShape g = plan(N, S, C, G, (int)es);
   float2* stat = static_cast<float2*>(ws);
   float* chan = reinterpret_cast<float*>(static_cast<char*>(ws) + up16((size_t)N * g.G * 8));

@@ -13,6 +13,7 @@
 // derived from one of them are common, so a quotient one ulp off would flip codes.
 #include <type_traits>
 
+#include "act_pairs.cuh"
 #include "gn_common.cuh"
 #include "gn_host.h"
 
@@ -63,56 +64,6 @@ __device__ __forceinline__ uint32_t code4(const float* v, float s, float i) {
     hi = fma2(fma2(hi, ns, b), ii, hi);
   }
   return code2(lo.x, lo.y) | code2(hi.x, hi.y) << 16;
-}
-
-// The activation and its derivative for values on their way to codes. The hardware tanh (error 2^-11) of
-// the bf16 epilogues would move one code in a hundred; on bf16 inputs the exponential and the divide are the
-// approximate ones (together about 1e-6), on fp32 inputs the accurate ones.
-__device__ __forceinline__ float ex2_ftz(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp_ftz(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-
-// sigmoid(2 u) of the tanh-GeLU's argument: (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
-__device__ __forceinline__ float2 gelu_u2(float2 z, float2 z2) {  // -2 u log2(e)
-  return mul2(z, fma2(z2, dup2(-2.0f * kLog2e * kGeluK * kGeluC), dup2(-2.0f * kLog2e * kGeluK)));
-}
-
-template <int EPI, bool FAST>
-__device__ __forceinline__ float2 q_act2(float2 z) {
-  if constexpr (!FAST || EPI == EPI_NONE) {
-    return make_float2(epi_fwd<EPI, false>(z.x), epi_fwd<EPI, false>(z.y));
-  } else {
-    const float2 t = EPI == EPI_SILU ? mul2(z, dup2(-kLog2e)) : gelu_u2(z, mul2(z, z));
-    const float2 d = add2(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), dup2(1.0f));
-    return mul2(z, make_float2(rcp_ftz(d.x), rcp_ftz(d.y)));
-  }
-}
-template <int EPI, bool FAST>
-__device__ __forceinline__ float2 q_grad2(float2 z) {
-  if constexpr (!FAST || EPI == EPI_NONE) {
-    return make_float2(epi_grad<EPI, false>(z.x), epi_grad<EPI, false>(z.y));
-  } else if constexpr (EPI == EPI_SILU) {  // s (1 + z (1 - s))
-    const float2 t = mul2(z, dup2(-kLog2e));
-    const float2 d = add2(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), dup2(1.0f));
-    const float2 s = make_float2(rcp_ftz(d.x), rcp_ftz(d.y));
-    return mul2(s, fma2(z, fma2(s, dup2(-1.0f), dup2(1.0f)), dup2(1.0f)));
-  } else {  // p = sigmoid(2 u): p (1 + z (1 - p) (2 u)'); 1 - p = a / (1 + a) without cancellation, a = exp(-|2 u|)
-    const float2 z2 = mul2(z, z), t = gelu_u2(z, z2);
-    const float2 a = make_float2(ex2_ftz(-fabsf(t.x)), ex2_ftz(-fabsf(t.y)));
-    const float2 d = add2(a, dup2(1.0f));
-    const float2 r = make_float2(rcp_ftz(d.x), rcp_ftz(d.y)), ra = mul2(r, a);
-    const float2 p = make_float2(t.x <= 0.0f ? r.x : ra.x, t.y <= 0.0f ? r.y : ra.y);
-    const float2 n = make_float2(t.x <= 0.0f ? ra.x : r.x, t.y <= 0.0f ? ra.y : r.y);
-    return mul2(p, fma2(mul2(z, n), fma2(z2, dup2(6.0f * kGeluK * kGeluC), dup2(2.0f * kGeluK)), dup2(1.0f)));
-  }
 }
 
 // The largest of each of K values over L lanes (K a power of two <= L): every step exchanges the half of the
@@ -319,7 +270,7 @@ __global__ void __launch_bounds__(32 * kWarpRows, 2)
         am[j] = 0.0f;
 #pragma unroll
         for (int e = 0; e < H; ++e) {
-          if constexpr (EPI != EPI_NONE) z[e] = q_act2<EPI, FAST>(z[e]);
+          if constexpr (EPI != EPI_NONE) z[e] = act_pair<EPI, FAST>(z[e]);
           f[j][2 * e] = z[e].x, f[j][2 * e + 1] = z[e].y;
           am[j] = max_nan(am[j], max_nan(fabsf(f[j][2 * e]), fabsf(f[j][2 * e + 1])));
         }
@@ -492,7 +443,7 @@ __global__ void __launch_bounds__(32 * kStageWarps, 1)
         }
 #pragma unroll
         for (int e = 0; e < H; ++e) {
-          if constexpr (EPI != EPI_NONE) z[e] = q_act2<EPI, FAST>(z[e]);
+          if constexpr (EPI != EPI_NONE) z[e] = act_pair<EPI, FAST>(z[e]);
           f[j][2 * e] = z[e].x, f[j][2 * e + 1] = z[e].y;
           am[j] = max_nan(am[j], max_nan(fabsf(z[e].x), fabsf(z[e].y)));
         }
@@ -633,7 +584,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_quant_row_kernel(c
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
       if constexpr (EPI != EPI_NONE) {
-        const float2 z = q_act2<EPI, FAST>(make_float2(f[k][e], f[k][e + 1]));
+        const float2 z = act_pair<EPI, FAST>(make_float2(f[k][e], f[k][e + 1]));
         f[k][e] = z.x, f[k][e + 1] = z.y;
       }
       am[k] = max_nan(am[k], max_nan(fabsf(f[k][e]), fabsf(f[k][e + 1])));
@@ -719,7 +670,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
       Vec<T>::unpack(rawd[i], d);
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
-        const float2 v = mul2(make_float2(d[e], d[e + 1]), q_grad2<EPI, FAST>(make_float2(f[i][e], f[i][e + 1])));
+        const float2 v = mul2(make_float2(d[e], d[e + 1]), act_grad_pair<EPI, FAST>(make_float2(f[i][e], f[i][e + 1])));
         f[i][e] = v.x, f[i][e + 1] = v.y;
       }
     }
