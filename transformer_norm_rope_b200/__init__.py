@@ -135,10 +135,16 @@ def check(status: int, where: str = "libgn") -> None:
 
 # ---------------------------------------------------------------- torch helpers
 
-def _torch():
-    import torch
+_TORCH = None
 
-    return torch
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+
+        _TORCH = torch
+    return _TORCH
 
 
 def _dt(t) -> int:
@@ -538,8 +544,14 @@ def _placed(f):
 
 def _rows16(x, name="x", like=None, dtype=None):
     """_rows, with the row stride of a matrix of one row or none (which nothing steps by) taken as
-    its width in whole 16 bytes."""
-    rows, hidden, ld = _rows(x, name, like=like, dtype=dtype)
+    its width in whole 16 bytes; a contiguous tensor needs no view of its rows made."""
+    n = x.numel()
+    if n and x.is_contiguous():
+        _need(x, name, like=like, dtype=dtype, contiguous=False)
+        hidden = ld = x.shape[-1] if x.dim() else 1
+        rows = n // hidden
+    else:
+        rows, hidden, ld = _rows(x, name, like=like, dtype=dtype)
     if rows <= 1:
         es = x.element_size()
         ld = (hidden * es + 15) // 16 * 16 // es
@@ -558,45 +570,85 @@ def _images(x, name="x", like=None, dtype=None):
     return N, S, C, ld
 
 
+# the outputs of the helpers below are made with empty_strided, the cheapest of torch's allocating calls: for
+# a single token the host's work, not the kernel, is what a call takes
+
+
+def _empty(shape, strides, dtype, device):
+    return _torch().empty_strided(shape, strides, dtype=dtype, device=device)
+
+
+_WORKSPACE = {}  # bytes by query, sizes and device
+
+
+def _workspace(query, name, device, *sizes):
+    """The workspace that `query` gives for these sizes on `device`, or None where it needs none, and its bytes."""
+    key = (name, device) + sizes
+    n = _WORKSPACE.get(key)
+    if n is None:
+        n = query(*sizes)
+        if len(_WORKSPACE) > 4096:
+            _WORKSPACE.clear()
+        _WORKSPACE[key] = n
+    return (_empty((n,), (1,), _torch().uint8, device) if n else None), n
+
+
+def _like_rows(x, ld):
+    """An output of x's shape and type and its row stride: x's own layout where it is contiguous in whole 16
+    bytes, else rows that start on 16-byte boundaries."""
+    if x.is_contiguous() and ld * x.element_size() % 16 == 0:
+        return _torch().empty_like(x), x.shape[-1]
+    es = x.element_size()
+    return empty_rows(x.shape, x.dtype, x.device), (x.shape[-1] * es + 15) // 16 * 16 // es
+
+
 @_placed
 def groupnorm_fwd(x, groups, w=None, b=None, eps=1e-5, epilogue="none", out=None, save_stats=True, stream=None):
     """GroupNorm of channels-last images x [N, ..., C] with an activation:
     y = epi((x - mean) * rstd * w + b), statistics over each image's groups of C / groups consecutive
     channels -> (y, mean [N, groups], rstd [N, groups]) (statistics fp32, or None)."""
-    torch = _torch()
+    f32 = _torch().float32
     N, S, Cn, ld = _images(x)
-    _need(w, "w", like=x, shape=(Cn,), dtype=x.dtype, optional=True)
-    _need(b, "b", like=x, shape=(Cn,), dtype=x.dtype, optional=True)
-    y = empty_rows(x.shape, x.dtype, x.device) if out is None else out
-    _need(y, "out", like=x, shape=x.shape, contiguous=False)
-    _, _, _, ldy = _images(y, "out", like=x, dtype=x.dtype)
-    mu, rs = torch.empty((2, N, groups), dtype=torch.float32, device=x.device).unbind(0) if save_stats else (None, None)
-    nws = gn_groupnorm_fwd_workspace(N, S, Cn, groups, _dt(x))
-    ws = torch.empty(nws, dtype=torch.uint8, device=x.device) if nws else None
-    check(gn_groupnorm_fwd(_ptr(x), _ptr(w), _ptr(b), _ptr(y), _ptr(mu), _ptr(rs), _ptr(ws), nws, N, S, Cn, groups, ld,
-                           ldy, eps, _epi(epilogue), _dt(x), _stream(stream)), "gn_groupnorm_fwd")
+    dtype, device = x.dtype, x.device
+    _need(w, "w", like=x, shape=(Cn,), dtype=dtype, optional=True)
+    _need(b, "b", like=x, shape=(Cn,), dtype=dtype, optional=True)
+    if out is None:
+        y, ldy = _like_rows(x, ld)
+    else:
+        y = out
+        _need(y, "out", like=x, shape=x.shape, contiguous=False)
+        _, _, _, ldy = _images(y, "out", like=x, dtype=dtype)
+    shape, strides, mu, rs = (N, groups), (groups, 1), None, None
+    if save_stats:
+        mu, rs = _empty(shape, strides, f32, device), _empty(shape, strides, f32, device)
+    dt = _dt(x)
+    ws, nws = _workspace(gn_groupnorm_fwd_workspace, "gn_fwd", device, N, S, Cn, groups, dt)
+    check(gn_groupnorm_fwd(x.data_ptr(), _ptr(w), _ptr(b), y.data_ptr(), _ptr(mu), _ptr(rs), _ptr(ws), nws, N, S, Cn,
+                           groups, ld, ldy, eps, _epi(epilogue), dt, _stream(stream)), "gn_groupnorm_fwd")
     return y, mu, rs
 
 
 @_placed
 def groupnorm_bwd(x, groups, w, b, mean, rstd, dy, epilogue="none", want_wgrad=True, stream=None):
     """Backward of groupnorm_fwd from its saved statistics -> (dx, dw, db) (dw, db fp32 or None)."""
-    torch = _torch()
+    f32 = _torch().float32
     N, S, Cn, ld = _images(x)
-    _need(w, "w", like=x, shape=(Cn,), dtype=x.dtype, optional=True)
-    _need(b, "b", like=x, shape=(Cn,), dtype=x.dtype, optional=True)
-    _need(mean, "mean", like=x, shape=(N, groups), dtype=torch.float32)
-    _need(rstd, "rstd", like=x, shape=(N, groups), dtype=torch.float32)
+    dtype, device = x.dtype, x.device
+    _need(w, "w", like=x, shape=(Cn,), dtype=dtype, optional=True)
+    _need(b, "b", like=x, shape=(Cn,), dtype=dtype, optional=True)
+    _need(mean, "mean", like=x, shape=(N, groups), dtype=f32)
+    _need(rstd, "rstd", like=x, shape=(N, groups), dtype=f32)
     _need(dy, "dy", like=x, shape=x.shape, contiguous=False)
-    _, _, _, lddy = _images(dy, "dy", like=x, dtype=x.dtype)
-    dx = empty_rows(x.shape, x.dtype, x.device)
-    _, _, _, lddx = _images(dx)
-    dw, db = torch.empty((2, Cn), dtype=torch.float32, device=x.device).unbind(0) if want_wgrad else (None, None)
-    nws = gn_groupnorm_bwd_workspace(N, S, Cn, groups, _dt(x))
-    ws = torch.empty(nws, dtype=torch.uint8, device=x.device) if nws else None
-    check(gn_groupnorm_bwd(_ptr(x), _ptr(w), _ptr(b), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(db),
-                           _ptr(ws), nws, N, S, Cn, groups, ld, lddy, lddx, _epi(epilogue), _dt(x), _stream(stream)),
-          "gn_groupnorm_bwd")
+    _, _, _, lddy = _images(dy, "dy", like=x, dtype=dtype)
+    dx, lddx = _like_rows(x, ld)
+    dw = db = None
+    if want_wgrad:
+        dw, db = _empty((Cn,), (1,), f32, device), _empty((Cn,), (1,), f32, device)
+    dt = _dt(x)
+    ws, nws = _workspace(gn_groupnorm_bwd_workspace, "gn_bwd", device, N, S, Cn, groups, dt)
+    check(gn_groupnorm_bwd(x.data_ptr(), _ptr(w), _ptr(b), mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), dx.data_ptr(),
+                           _ptr(dw), _ptr(db), _ptr(ws), nws, N, S, Cn, groups, ld, lddy, lddx, _epi(epilogue), dt,
+                           _stream(stream)), "gn_groupnorm_bwd")
     return dx, dw, db
 
 
@@ -608,8 +660,9 @@ def _blocks(n):
 
 
 def _codes(rows, cols, device):
-    """uninitialised codes [rows, cols] and their row stride"""
-    return empty_rows((rows, cols), _torch().float8_e4m3fn, device), (cols + 15) // 16 * 16
+    """uninitialised codes [rows, cols], rows on 16-byte boundaries, and their row stride"""
+    ld = (cols + 15) // 16 * 16
+    return _empty((rows, cols), (ld, 1), _torch().float8_e4m3fn, device), ld
 
 
 @_placed
@@ -617,19 +670,18 @@ def norm_quant_fp8(x, g=None, beta=None, eps=1e-6, norm="rms", gemma=False, epil
     """epi(norm(x)) of the rows of x [..., hidden] in 8 bits, one scale per 128 values of a row ->
     (codes [rows, hidden] float8_e4m3fn, scales [rows, ceil(hidden / 128)] fp32, mean, rstd) (statistics
     fp32 [rows], None where the norm has none)."""
-    torch = _torch()
+    f32 = _torch().float32
     rows, hidden, ld = _rows16(x)
-    kind = _norm(norm)
-    _need(g, "g", like=x, shape=(hidden,), dtype=x.dtype, optional=True)
-    _need(beta, "beta", like=x, shape=(hidden,), dtype=x.dtype, optional=True)
-    f32, device = torch.float32, x.device
+    dtype, device, kind = x.dtype, x.device, _norm(norm)
+    _need(g, "g", like=x, shape=(hidden,), dtype=dtype, optional=True)
+    _need(beta, "beta", like=x, shape=(hidden,), dtype=dtype, optional=True)
     q, ldq = _codes(rows, hidden, device)
     nb = _blocks(hidden)
-    s = torch.empty((rows, nb), dtype=f32, device=device)
-    mu = torch.empty(rows, dtype=f32, device=device) if save_stats and kind == GN_NORM_LN else None
-    rs = torch.empty(rows, dtype=f32, device=device) if save_stats and kind != GN_NORM_NONE else None
-    check(gn_norm_quant_fp8(_ptr(x), _ptr(g), _ptr(beta), _ptr(q), _ptr(s), _ptr(mu), _ptr(rs), rows, hidden, ld,
-                            ldq, nb, eps, kind, int(gemma), _epi(epilogue), _dt(x), _stream(stream)),
+    s = _empty((rows, nb), (nb, 1), f32, device)
+    mu = _empty((rows,), (1,), f32, device) if save_stats and kind == GN_NORM_LN else None
+    rs = _empty((rows,), (1,), f32, device) if save_stats and kind != GN_NORM_NONE else None
+    check(gn_norm_quant_fp8(x.data_ptr(), _ptr(g), _ptr(beta), q.data_ptr(), s.data_ptr(), _ptr(mu), _ptr(rs), rows, hidden,
+                            ld, ldq, nb, eps, kind, int(gemma), _epi(epilogue), _dt(x), _stream(stream)),
           "gn_norm_quant_fp8")
     return q, s, mu, rs
 
@@ -641,8 +693,7 @@ def _ld(t):
 
 @_placed
 def _quant_fp8(x, dy, tile, by_rows, transposed, want_db, epilogue, stream=None):
-    torch = _torch()
-    _need(x, "x", contiguous=False)
+    f32 = _torch().float32
     if x.dim() != 2:
         raise ValueError("x must be [rows, cols]")
     rows, cols, ld = _rows16(x)
@@ -650,16 +701,16 @@ def _quant_fp8(x, dy, tile, by_rows, transposed, want_db, epilogue, stream=None)
     if dy is not None:
         _need(dy, "dy", like=x, shape=x.shape, contiguous=False)
         _, _, lddy = _rows16(dy, "dy", like=x, dtype=x.dtype)
-    mk = (lambda r, c: torch.empty((r, c), dtype=torch.float32, device=x.device))
-    rb, cb = _blocks(rows), _blocks(cols)
-    q, ldq = _codes(rows, cols, x.device) if by_rows else (None, 0)
-    s = mk(rb if tile else rows, cb) if by_rows else None
-    qt, ldqt = _codes(cols, rows, x.device) if transposed else (None, 0)
-    st = mk(cb if tile else cols, rb) if transposed else None
-    db = torch.empty(cols, dtype=torch.float32, device=x.device) if want_db else None
-    nws = gn_quant_fp8_workspace(rows, cols) if want_db else 0
-    ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=x.device) if want_db else None
-    check(gn_quant_fp8(_ptr(x), _ptr(dy), _ptr(q), _ptr(s), _ptr(qt), _ptr(st), _ptr(db), _ptr(ws), nws, rows, cols, ld,
+    device, rb, cb = x.device, _blocks(rows), _blocks(cols)
+    q, ldq = _codes(rows, cols, device) if by_rows else (None, 0)
+    s = _empty((rb if tile else rows, cb), (cb, 1), f32, device) if by_rows else None
+    qt, ldqt = _codes(cols, rows, device) if transposed else (None, 0)
+    st = _empty((cb if tile else cols, rb), (rb, 1), f32, device) if transposed else None
+    db, ws, nws = None, None, 0
+    if want_db:
+        db = _empty((cols,), (1,), f32, device)
+        ws, nws = _workspace(gn_quant_fp8_workspace, "quant", device, rows, cols)
+    check(gn_quant_fp8(x.data_ptr(), _ptr(dy), _ptr(q), _ptr(s), _ptr(qt), _ptr(st), _ptr(db), _ptr(ws), nws, rows, cols, ld,
                        lddy, ldq, cb, ldqt, rb, GN_FP8_TILE if tile else GN_FP8_VEC, _epi(epilogue), _dt(x),
                        _stream(stream)), "gn_quant_fp8")
     return q, s, qt, st, db
@@ -689,31 +740,35 @@ def linear_fp8(a, sa, b, sb, d=None, epilogue="none", out=None, out_dtype=None, 
     [M, ceil(K / 128)] and sb [ceil(N / 128), ceil(K / 128)] (128 x 128 blocks) or [N, ceil(K / 128)]. y is
     bf16, or fp32 (out_dtype float32: no activation; accumulate adds to `out`)."""
     torch = _torch()
-    _, _, lda = _rows16(a, "a", dtype=torch.float8_e4m3fn)
-    _, _, ldb = _rows16(b, "b", like=a, dtype=torch.float8_e4m3fn)
+    f8, f32 = torch.float8_e4m3fn, torch.float32
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
         raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} must be [M, K] and [N, K]")
+    _, _, lda = _rows16(a, "a", dtype=f8)
+    _, _, ldb = _rows16(b, "b", like=a, dtype=f8)
     (M, K), N = a.shape, b.shape[0]
     nb, kb = _blocks(N), _blocks(K)
-    _need(sa, "sa", like=a, shape=(M, kb), dtype=torch.float32, contiguous=False)
-    _need(sb, "sb", like=a, dtype=torch.float32, contiguous=False)
+    _need(sa, "sa", like=a, shape=(M, kb), dtype=f32, contiguous=False)
+    _need(sb, "sb", like=a, dtype=f32, contiguous=False)
     if tuple(sb.shape) not in ((nb, kb), (N, kb)):
         raise ValueError(f"sb has shape {tuple(sb.shape)}, expected {(nb, kb)} or {(N, kb)}")
     for t, name in ((sa, "sa"), (sb, "sb")):
-        if t.numel() and t.stride(-1) != 1 and t.shape[1] > 1:
+        if t.stride(-1) != 1 and t.numel() and kb > 1:
             raise ValueError(f"last dimension of {name} must be contiguous")
-    _need(d, "d", like=a, shape=(N,), dtype=torch.float32, optional=True)
+    _need(d, "d", like=a, shape=(N,), dtype=f32, optional=True)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        y = empty_rows((M, N), out_dtype or torch.bfloat16, a.device)
+        dtype = out_dtype or torch.bfloat16
+        per = 16 // dtype.itemsize
+        ldy = (N + per - 1) // per * per
+        y = _empty((M, N), (ldy, 1), dtype, a.device)
     else:
         y = out
-    _need(y, "out", like=a, shape=(M, N), contiguous=False)
-    _, _, ldy = _rows16(y, "out", like=a, dtype=out_dtype or y.dtype)
-    check(gn_linear_fp8(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(d), _ptr(y), M, N, K, lda, _ld(sa), ldb, _ld(sb),
-                        ldy, FP8_BLOCK if sb.shape[0] == nb else 1, int(accumulate), _epi(epilogue), _dt(y),
-                        _stream(stream)), "gn_linear_fp8")
+        _need(y, "out", like=a, shape=(M, N), contiguous=False)
+        _, _, ldy = _rows16(y, "out", like=a, dtype=out_dtype or y.dtype)
+    check(gn_linear_fp8(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), _ptr(d), y.data_ptr(), M, N, K, lda,
+                        _ld(sa), ldb, _ld(sb), ldy, FP8_BLOCK if sb.shape[0] == nb else 1, int(accumulate),
+                        _epi(epilogue), _dt(y), _stream(stream)), "gn_linear_fp8")
     return y
 
 

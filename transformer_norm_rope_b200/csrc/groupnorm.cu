@@ -17,6 +17,8 @@
 // walks down the positions, so its per-channel sums and parameters stay in registers and every warp
 // access covers whole runs of a row. The forward's sums are (mean, centred sum of squares) per
 // channel, batch by batch with Chan's update: no E[x^2] - E[x]^2 cancellation.
+#include <type_traits>
+
 #include "act_pairs.cuh"
 #include "gn_common.cuh"
 #include "gn_host.h"
@@ -25,7 +27,7 @@ namespace gn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // positions a thread has in flight
+constexpr int kBatch = 8;  // positions a thread has in flight in the forward's sums; half of it elsewhere
 
 struct GnShape {
   int64_t S;       // positions of an image
@@ -89,49 +91,65 @@ struct Place {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const T* __restrict__ x, int64_t ldx, GnShape g,
                                                             float2* __restrict__ part) {
-  constexpr int E = Vec<T>::N;
+  constexpr int E = Vec<T>::N, H = E / 2;
   __shared__ float sm_mean[kThreads * E];
   __shared__ float sm_m2[kThreads * E];
   __shared__ float sm_cnt[kThreads];
   const Place p = Place::make<E>(g);
-  float mean[E], m2[E], cnt = 0.0f;
+  float2 mean2[H], m22[H];
+  float cnt = 0.0f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) mean[e] = 0.0f, m2[e] = 0.0f;
-  if (p.active) {
-    const T* img = x + (int64_t)p.n * g.S * ldx;
-    for (int64_t r = p.r0 + p.lane_row; r < p.r1; r += (int64_t)g.rl * kBatch) {
-      float f[kBatch][E];
-      int k = 0;
+  for (int e = 0; e < H; ++e) mean2[e] = m22[e] = make_float2(0.0f, 0.0f);
+  // B positions: their mean and centred squares per channel, merged with what there is (Chan)
+  auto merge = [&](const uint4* u, auto size) {
+    constexpr int B = decltype(size)::value;
+    const float tot = cnt + B, fr = B / tot, wt = cnt * fr;
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int64_t rr = r + (int64_t)j * g.rl;
-        if (rr < p.r1) {
-          load_vec<T>(img + rr * ldx, p.v, g.C, p.whole, f[j]);
-          k = j + 1;
-        } else {
+    for (int e = 0; e < H; ++e) {
+      float2 f[B], t = make_float2(0.0f, 0.0f), q = t;
 #pragma unroll
-          for (int e = 0; e < E; ++e) f[j][e] = 0.0f;
-        }
+      for (int k = 0; k < B; ++k) {
+        float2 all[H];
+        unpack2<T>(u[k], all);
+        f[k] = all[e];
+        t = add2(t, f[k]);
       }
-      const float nk = (float)k, inv = 1.0f / nk, tot = cnt + nk;
-      const float fr = nk / tot, w = cnt * fr;  // Chan: weights of the batch and of the square
+      const float2 bm = mul2(t, dup2(1.0f / B)), nm = mul2(t, dup2(-1.0f / B));
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float t = 0.0f, q = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) t += f[j][e];
-        const float bm = t * inv;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const float d = j < k ? f[j][e] - bm : 0.0f;
-          q = fmaf(d, d, q);
-        }
-        const float dl = bm - mean[e];
-        mean[e] = fmaf(dl, fr, mean[e]);
-        m2[e] += fmaf(dl * dl, w, q);
+      for (int k = 0; k < B; ++k) {
+        const float2 d = add2(f[k], nm);
+        q = fma2(d, d, q);
       }
-      cnt = tot;
+      const float2 dl = add2(bm, mul2(mean2[e], dup2(-1.0f)));
+      mean2[e] = fma2(dl, dup2(fr), mean2[e]);
+      m22[e] = add2(m22[e], fma2(mul2(dl, dl), dup2(wt), q));
     }
+    cnt = tot;
+  };
+  if (p.active) {
+    const T* row = x + ((int64_t)p.n * g.S + p.r0 + p.lane_row) * ldx;
+    const int64_t step = (int64_t)g.rl * ldx;
+    int64_t left = (p.r1 - p.r0 - p.lane_row + g.rl - 1) / g.rl;  // positions of this thread
+    if (p.whole) {
+      for (; left >= kBatch; left -= kBatch, row += kBatch * step) {
+        uint4 u[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) u[k] = *reinterpret_cast<const uint4*>(row + k * step + p.v * E);
+        merge(u, std::integral_constant<int, kBatch>{});
+      }
+    }
+    for (; left > 0; --left, row += step) {
+      float f[E];
+      load_vec<T>(row, p.v, g.C, p.whole, f);
+      const uint4 u = Vec<T>::pack(f);
+      merge(&u, std::integral_constant<int, 1>{});
+    }
+  }
+  float mean[E], m2[E];
+#pragma unroll
+  for (int e = 0; e < H; ++e) {
+    mean[2 * e] = mean2[e].x, mean[2 * e + 1] = mean2[e].y;
+    m2[2 * e] = m22[e].x, m2[2 * e + 1] = m22[e].y;
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sm_mean[threadIdx.x * E + e] = mean[e], sm_m2[threadIdx.x * E + e] = m2[e];
@@ -166,28 +184,38 @@ __device__ __forceinline__ float block_sum(float v, float* red) {  // kThreads t
   return t;
 }
 
-// one block per (image, group): joins the slabs and the group's channels
+// one block per (image, group): joins the slabs and the group's channels. A thread takes every `parts`-th
+// slab of one channel (parts = kThreads / P, one where the group is wider).
 __global__ void __launch_bounds__(kThreads) gn_stats_join_kernel(const float2* __restrict__ part, GnShape g, float eps,
                                                                  float2* __restrict__ stat, float* __restrict__ mean,
                                                                  float* __restrict__ rstd) {
   __shared__ float red[kThreads / 32];
+  pdl_wait();
   const int n = blockIdx.x / g.G, gr = blockIdx.x % g.G;
   const float2* base = part + (int64_t)n * g.chunks * g.C + (int64_t)gr * g.P;
-  const int64_t items = (int64_t)g.chunks * g.P;
-  auto count = [&](int64_t i) {
-    const int64_t r0 = (i / g.P) * g.rows;
-    return (float)((r0 + g.rows < g.S ? r0 + g.rows : g.S) - r0);
+  const int parts = g.P < kThreads ? kThreads / g.P : 1;
+  const int c0 = g.P < kThreads ? (int)threadIdx.x % g.P : (int)threadIdx.x;
+  const int k0 = g.P < kThreads ? (int)threadIdx.x / g.P : 0;
+  auto count = [&](int k) {
+    const int64_t r0 = (int64_t)k * g.rows;
+    return (float)(g.S - r0 < g.rows ? g.S - r0 : g.rows);
   };
   float t = 0.0f;
-  for (int64_t i = threadIdx.x; i < items; i += kThreads) t = fmaf(count(i), base[(i / g.P) * g.C + i % g.P].x, t);
+  if (k0 < parts)
+    for (int c = c0; c < g.P; c += kThreads)
+#pragma unroll 4
+      for (int k = k0; k < g.chunks; k += parts) t = fmaf(count(k), base[(int64_t)k * g.C + c].x, t);
   const float total = (float)((double)g.S * g.P);
   const float mu = block_sum(t, red) / total;
   float q = 0.0f;
-  for (int64_t i = threadIdx.x; i < items; i += kThreads) {
-    const float2 v = base[(i / g.P) * g.C + i % g.P];
-    const float d = v.x - mu;
-    q += fmaf(count(i) * d, d, v.y);
-  }
+  if (k0 < parts)
+    for (int c = c0; c < g.P; c += kThreads)
+#pragma unroll 4
+      for (int k = k0; k < g.chunks; k += parts) {
+        const float2 v = base[(int64_t)k * g.C + c];
+        const float d = v.x - mu;
+        q += fmaf(count(k) * d, d, v.y);
+      }
   const float var = block_sum(q, red) / total;
   if (threadIdx.x == 0) {
     const float s = 1.0f / sqrtf(var + eps);
@@ -206,6 +234,7 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(const T* x, int64_t 
   constexpr bool FAST = fast_math_for<T>();
   const Place p = Place::make<E>(g);
   if (!p.active) return;
+  pdl_wait();
   float mu[E], a[E], sh[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -219,16 +248,40 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(const T* x, int64_t 
       mu[e] = a[e] = sh[e] = 0.0f;
     }
   }
-  const int64_t img = (int64_t)p.n * g.S;
-  for (int64_t r = p.r0 + p.lane_row; r < p.r1; r += g.rl) {
-    float f[E];
-    load_vec<T>(x + (img + r) * ldx, p.v, g.C, p.whole, f);
+  float2 nmu[E / 2], a2[E / 2], sh2[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 z = act_pair<EPI, FAST>(make_float2(fmaf(f[e] - mu[e], a[e], sh[e]), fmaf(f[e + 1] - mu[e + 1], a[e + 1], sh[e + 1])));
-      f[e] = z.x, f[e + 1] = z.y;
+  for (int e = 0; e < E / 2; ++e) {
+    nmu[e] = make_float2(-mu[2 * e], -mu[2 * e + 1]);
+    a2[e] = make_float2(a[2 * e], a[2 * e + 1]);
+    sh2[e] = make_float2(sh[2 * e], sh[2 * e + 1]);
+  }
+  // the slab from its end: what the sums read last is still in L2
+  const int64_t img = (int64_t)p.n * g.S;
+  int64_t left = (p.r1 - p.r0 - p.lane_row + g.rl - 1) / g.rl;  // positions of this thread
+  auto one = [&](const uint4& u) {
+    float2 f[E / 2];
+    unpack2<T>(u, f);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) f[e] = act_pair<EPI, FAST>(fma2(add2(f[e], nmu[e]), a2[e], sh2[e]));
+    return pack2<T>(f);
+  };
+  if (p.whole) {
+    constexpr int B = kBatch / 2;
+    for (; left >= B; left -= B) {
+      uint4 u[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k)
+        u[k] = ld_stream(x + (img + p.r0 + p.lane_row + (left - 1 - k) * g.rl) * ldx + p.v * E);
+#pragma unroll
+      for (int k = 0; k < B; ++k) st_stream(y + (img + p.r0 + p.lane_row + (left - 1 - k) * g.rl) * ldy + p.v * E, one(u[k]));
     }
-    store_vec<T>(y + (img + r) * ldy, p.v, g.C, p.whole, f);
+  }
+  for (; left > 0; --left) {
+    const int64_t r = img + p.r0 + p.lane_row + (left - 1) * g.rl;
+    float f[E];
+    load_vec<T>(x + r * ldx, p.v, g.C, p.whole, f);
+    Vec<T>::unpack(one(Vec<T>::pack(f)), f);
+    store_vec<T>(y + r * ldy, p.v, g.C, p.whole, f);
   }
 }
 
@@ -246,9 +299,11 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const T* __restri
   __shared__ float sm_a[kThreads * E];
   __shared__ float sm_b[kThreads * E];
   const Place p = Place::make<E>(g);
+  constexpr int H = E / 2;
   float A[E], B[E];
+  float2 A2[H], B2[H];
 #pragma unroll
-  for (int e = 0; e < E; ++e) A[e] = 0.0f, B[e] = 0.0f;
+  for (int e = 0; e < H; ++e) A2[e] = B2[e] = make_float2(0.0f, 0.0f);
   if (p.active) {
     float mu[E], s[E], wf[E], bf[E];
 #pragma unroll
@@ -260,20 +315,52 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const T* __restri
       wf[e] = in ? ld_param(w, c, 1.0f) : 0.0f;
       bf[e] = in ? ld_param(b, c, 0.0f) : 0.0f;
     }
-    const int64_t img = (int64_t)p.n * g.S;
-    for (int64_t r = p.r0 + p.lane_row; r < p.r1; r += g.rl) {
-      float f[E], d[E];
-      load_vec<T>(x + (img + r) * ldx, p.v, g.C, p.whole, f);
-      load_vec<T>(dy + (img + r) * lddy, p.v, g.C, p.whole, d);
+    float2 nmu[H], s2[H], w2[H], b2[H];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 xh = make_float2((f[e] - mu[e]) * s[e], (f[e + 1] - mu[e + 1]) * s[e + 1]);
-        const float2 gr = act_grad_pair<EPI, FAST>(make_float2(fmaf(xh.x, wf[e], bf[e]), fmaf(xh.y, wf[e + 1], bf[e + 1])));
-        const float g0 = d[e] * gr.x, g1 = d[e + 1] * gr.y;
-        A[e] += g0, A[e + 1] += g1;
-        B[e] = fmaf(g0, xh.x, B[e]), B[e + 1] = fmaf(g1, xh.y, B[e + 1]);
+    for (int e = 0; e < H; ++e) {
+      nmu[e] = make_float2(-mu[2 * e], -mu[2 * e + 1]);
+      s2[e] = make_float2(s[2 * e], s[2 * e + 1]);
+      w2[e] = make_float2(wf[2 * e], wf[2 * e + 1]);
+      b2[e] = make_float2(bf[2 * e], bf[2 * e + 1]);
+    }
+    auto one = [&](const uint4& ux, const uint4& ud) {
+      float2 f[H], d[H];
+      unpack2<T>(ux, f);
+      unpack2<T>(ud, d);
+#pragma unroll
+      for (int e = 0; e < H; ++e) {
+        const float2 xh = mul2(add2(f[e], nmu[e]), s2[e]);
+        const float2 gg = EPI == EPI_NONE ? d[e] : mul2(d[e], act_grad_pair<EPI, FAST>(fma2(xh, w2[e], b2[e])));
+        A2[e] = add2(A2[e], gg);
+        B2[e] = fma2(gg, xh, B2[e]);
+      }
+    };
+    const int64_t row0 = (int64_t)p.n * g.S + p.r0 + p.lane_row;
+    int64_t left = (p.r1 - p.r0 - p.lane_row + g.rl - 1) / g.rl, r = row0;
+    if (p.whole) {
+      constexpr int B = kBatch / 2;
+      for (; left >= B; left -= B, r += B * g.rl) {
+        uint4 ux[B], ud[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+          ux[k] = *reinterpret_cast<const uint4*>(x + (r + k * g.rl) * ldx + p.v * E);
+          ud[k] = *reinterpret_cast<const uint4*>(dy + (r + k * g.rl) * lddy + p.v * E);
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) one(ux[k], ud[k]);
       }
     }
+    for (; left > 0; --left, r += g.rl) {
+      float f[E], d[E];
+      load_vec<T>(x + r * ldx, p.v, g.C, p.whole, f);
+      load_vec<T>(dy + r * lddy, p.v, g.C, p.whole, d);
+      one(Vec<T>::pack(f), Vec<T>::pack(d));
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < H; ++e) {
+    A[2 * e] = A2[e].x, A[2 * e + 1] = A2[e].y;
+    B[2 * e] = B2[e].x, B[2 * e + 1] = B2[e].y;
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sm_a[threadIdx.x * E + e] = A[e], sm_b[threadIdx.x * E + e] = B[e];
@@ -297,21 +384,32 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_join_kernel(const float2* __r
                                                                const T* __restrict__ w, GnShape g,
                                                                float* __restrict__ chan, float2* __restrict__ stat) {
   __shared__ float red[kThreads / 32];
+  __shared__ float2 sums[kThreads];
+  pdl_wait();
   const int n = blockIdx.x / g.G, gr = blockIdx.x % g.G;
   float m1 = 0.0f, m2 = 0.0f;
-  for (int j = threadIdx.x; j < g.P; j += kThreads) {
-    const int c = gr * g.P + j;
-    float ta = 0.0f, tb = 0.0f;
-    for (int k = 0; k < g.chunks; ++k) {
-      const float2 v = part[((int64_t)n * g.chunks + k) * g.C + c];
-      ta += v.x;
-      tb += v.y;
+  const int parts = g.P < kThreads ? kThreads / g.P : 1;
+  for (int b0 = 0; b0 < g.P; b0 += kThreads) {  // a thread: every `parts`-th slab of one channel
+    const int j = g.P < kThreads ? (int)threadIdx.x % g.P : b0 + (int)threadIdx.x;
+    const int k0 = g.P < kThreads ? (int)threadIdx.x / g.P : 0;
+    float2 t = make_float2(0.0f, 0.0f);
+    if (j < g.P && k0 < parts) {
+      const float2* src = part + (int64_t)n * g.chunks * g.C + gr * g.P + j;
+#pragma unroll 4
+      for (int k = k0; k < g.chunks; k += parts) t = add2(t, src[(int64_t)k * g.C]);
     }
-    chan[(int64_t)n * 2 * g.C + c] = tb;
-    chan[(int64_t)n * 2 * g.C + g.C + c] = ta;
-    const float wc = ld_param(w, c, 1.0f);
-    m1 = fmaf(wc, ta, m1);
-    m2 = fmaf(wc, tb, m2);
+    sums[threadIdx.x] = t;
+    __syncthreads();
+    if (j < g.P && k0 == 0) {
+      for (int k = 1; k < parts; ++k) t = add2(t, sums[k * g.P + j]);
+      const int c = gr * g.P + j;
+      chan[(int64_t)n * 2 * g.C + c] = t.y;
+      chan[(int64_t)n * 2 * g.C + g.C + c] = t.x;
+      const float wc = ld_param(w, c, 1.0f);
+      m1 = fmaf(wc, t.x, m1);
+      m2 = fmaf(wc, t.y, m2);
+    }
+    __syncthreads();
   }
   const float inv = 1.0f / (float)((double)g.S * g.P);
   m1 = block_sum(m1, red) * inv;
@@ -330,6 +428,7 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_apply_kernel(const T* __restr
   constexpr bool FAST = fast_math_for<T>();
   const Place p = Place::make<E>(g);
   if (!p.active) return;
+  pdl_wait();
   float mu[E], s[E], wf[E], bf[E], m1[E], m2[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -343,19 +442,52 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_apply_kernel(const T* __restr
     wf[e] = in ? ld_param(w, c, 1.0f) : 0.0f;
     bf[e] = in ? ld_param(b, c, 0.0f) : 0.0f;
   }
-  const int64_t img = (int64_t)p.n * g.S;
-  for (int64_t r = p.r0 + p.lane_row; r < p.r1; r += g.rl) {
-    float f[E], d[E];
-    load_vec<T>(x + (img + r) * ldx, p.v, g.C, p.whole, f);
-    load_vec<T>(dy + (img + r) * lddy, p.v, g.C, p.whole, d);
+  constexpr int H = E / 2;
+  float2 nmu[H], s2[H], w2[H], b2[H], n1[H], n2[H];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 xh = make_float2((f[e] - mu[e]) * s[e], (f[e + 1] - mu[e + 1]) * s[e + 1]);
-      const float2 gr = act_grad_pair<EPI, FAST>(make_float2(fmaf(xh.x, wf[e], bf[e]), fmaf(xh.y, wf[e + 1], bf[e + 1])));
-      f[e] = s[e] * (fmaf(d[e] * gr.x, wf[e], -m1[e]) - xh.x * m2[e]);
-      f[e + 1] = s[e + 1] * (fmaf(d[e + 1] * gr.y, wf[e + 1], -m1[e + 1]) - xh.y * m2[e + 1]);
+  for (int e = 0; e < H; ++e) {
+    nmu[e] = make_float2(-mu[2 * e], -mu[2 * e + 1]);
+    s2[e] = make_float2(s[2 * e], s[2 * e + 1]);
+    w2[e] = make_float2(wf[2 * e], wf[2 * e + 1]);
+    b2[e] = make_float2(bf[2 * e], bf[2 * e + 1]);
+    n1[e] = make_float2(-m1[2 * e], -m1[2 * e + 1]);
+    n2[e] = make_float2(-m2[2 * e], -m2[2 * e + 1]);
+  }
+  auto one = [&](const uint4& ux, const uint4& ud) {
+    float2 f[H], d[H];
+    unpack2<T>(ux, f);
+    unpack2<T>(ud, d);
+#pragma unroll
+    for (int e = 0; e < H; ++e) {
+      const float2 xh = mul2(add2(f[e], nmu[e]), s2[e]);
+      const float2 gg = EPI == EPI_NONE ? d[e] : mul2(d[e], act_grad_pair<EPI, FAST>(fma2(xh, w2[e], b2[e])));
+      f[e] = mul2(s2[e], fma2(xh, n2[e], fma2(gg, w2[e], n1[e])));
     }
-    store_vec<T>(dx + (img + r) * lddx, p.v, g.C, p.whole, f);
+    return pack2<T>(f);
+  };
+  // the slab from its end: what the sums read last is still in L2
+  const int64_t row0 = (int64_t)p.n * g.S + p.r0 + p.lane_row;
+  int64_t left = (p.r1 - p.r0 - p.lane_row + g.rl - 1) / g.rl;
+  if (p.whole) {
+    constexpr int B = kBatch / 4;
+    for (; left >= B; left -= B) {
+      uint4 ux[B], ud[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        ux[k] = ld_stream(x + (row0 + (left - 1 - k) * g.rl) * ldx + p.v * E);
+        ud[k] = ld_stream(dy + (row0 + (left - 1 - k) * g.rl) * lddy + p.v * E);
+      }
+#pragma unroll
+      for (int k = 0; k < B; ++k) st_stream(dx + (row0 + (left - 1 - k) * g.rl) * lddx + p.v * E, one(ux[k], ud[k]));
+    }
+  }
+  for (; left > 0; --left) {
+    const int64_t r = row0 + (left - 1) * g.rl;
+    float f[E], d[E];
+    load_vec<T>(x + r * ldx, p.v, g.C, p.whole, f);
+    load_vec<T>(dy + r * lddy, p.v, g.C, p.whole, d);
+    Vec<T>::unpack(one(Vec<T>::pack(f), Vec<T>::pack(d)), f);
+    store_vec<T>(dx + r * lddx, p.v, g.C, p.whole, f);
   }
 }
 
@@ -375,6 +507,8 @@ struct Bundle {
   int bv;       // its 16-byte vectors
   int bundles;  // of an image
   int cs;       // blocks of a cluster
+  int rows;     // positions of a block (the last ones may have fewer)
+  int lp;       // log2 of the lanes that take different channels of a group in a warp's sum
 };
 
 template <int N>
@@ -409,7 +543,7 @@ template <int E>
 struct ResPlace {
   int n, c0, nch, lv, lr, rl, rank;
   bool active;
-  int64_t r0, r1;
+  int r0, r1;
   __device__ __forceinline__ ResPlace(const Bundle& g) {
     rank = (int)cluster_rank_();
     const int unit = blockIdx.x / g.cs;
@@ -420,8 +554,8 @@ struct ResPlace {
     lr = threadIdx.x / g.bv;
     lv = threadIdx.x % g.bv;
     active = lr < rl && lv * E < nch;
-    r0 = g.S * rank / g.cs;
-    r1 = g.S * (rank + 1) / g.cs;
+    r0 = (int)(g.S < (int64_t)rank * g.rows ? g.S : rank * g.rows);
+    r1 = (int)(g.S - r0 < g.rows ? g.S : r0 + g.rows);
   }
 };
 
@@ -432,7 +566,7 @@ __device__ __forceinline__ void res_load(uint4 (&raw)[VPT], const T* x, int64_t 
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     raw[k] = make_uint4(0, 0, 0, 0);
-    if (p.active && p.r0 + p.lr + (int64_t)k * p.rl < p.r1) raw[k] = ld_stream(base + (int64_t)k * p.rl * ld);
+    if (p.active && p.r0 + p.lr + k * p.rl < p.r1) raw[k] = ld_stream(base + (int64_t)k * p.rl * ld);
   }
 }
 
@@ -472,9 +606,12 @@ __device__ __forceinline__ int res_parts(const float (&v)[NQ][E], float* red, in
   return parts;
 }
 
-__device__ __forceinline__ float warp_sum_of(const float* red, int W, int parts, int ch0, int P, int lane) {
+// the sum over a group's channels (from ch0, P of them) and the parts, by one warp: 2^lp lanes take different
+// channels, the others different parts
+__device__ __forceinline__ float warp_sum_of(const float* red, int W, int parts, int ch0, int P, int lp, int lane) {
   float t = 0.0f;
-  for (int i = lane; i < P * parts; i += 32) t += red[(i / P) * W + ch0 + i % P];
+  for (int c = lane & ((1 << lp) - 1); c < P; c += 1 << lp)
+    for (int k = lane >> lp; k < parts; k += 32 >> lp) t += red[k * W + ch0 + c];
   return group_sum<32>(t);
 }
 
@@ -495,7 +632,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
   const int ng = p.nch / g.P;
   uint4 raw[VPT];
   res_load<T, VPT>(raw, x, ldx, p, g.S);
-  const float cnt = (float)((p.r1 - p.r0) * g.P), inv_cnt = cnt > 0.0f ? 1.0f / cnt : 0.0f;
+  const float cnt = (float)(p.r1 - p.r0) * (float)g.P, inv_cnt = cnt > 0.0f ? 1.0f / cnt : 0.0f;
   {
     float s[1][E];
 #pragma unroll
@@ -509,7 +646,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
     }
     const int parts = res_parts<E, 1>(s, red, W, p.rl, p.lr < p.rl);
     for (int i = warp; i < ng; i += kResThreads / 32) {
-      const float t = warp_sum_of(red, W, parts, i * g.P, g.P, lane);
+      const float t = warp_sum_of(red, W, parts, i * g.P, g.P, g.lp, lane);
       if (lane == 0) own[i].x = t * inv_cnt;
     }
     __syncthreads();
@@ -522,7 +659,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
     }
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (p.r0 + p.lr + (int64_t)k * p.rl < p.r1) {
+      if (p.r0 + p.lr + k * p.rl < p.r1) {
         float f[E];
         Vec<T>::unpack(raw[k], f);
 #pragma unroll
@@ -531,7 +668,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
     }
     const int parts2 = res_parts<E, 1>(s, red, W, p.rl, p.lr < p.rl);
     for (int i = warp; i < ng; i += kResThreads / 32) {
-      const float t = warp_sum_of(red, W, parts2, i * g.P, g.P, lane);
+      const float t = warp_sum_of(red, W, parts2, i * g.P, g.P, g.lp, lane);
       if (lane == 0) own[i].y = t;
     }
     keep_packed(raw);
@@ -547,14 +684,23 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
     float mu, q = 0.0f;
     if (g.cs > 1) {  // join the blocks' statistics in rank order
       float t = 0.0f;
-      for (int r = 0; r < g.cs; ++r)
-        t = fmaf((float)((g.S * (r + 1) / g.cs - g.S * r / g.cs) * g.P), peer_f2(own + i, r).x, t);
+      float2 v[8];
+      auto count = [&](int r) {
+        const int left = (int)g.S - r * g.rows;
+        return left <= 0 ? 0.0f : (float)(left < g.rows ? left : g.rows) * (float)g.P;
+      };
+#pragma unroll
+      for (int r = 0; r < 8; ++r) v[r] = r < g.cs ? peer_f2(own + i, r) : make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < g.cs) t = fmaf(count(r), v[r].x, t);
       mu = t / total;
-      for (int r = 0; r < g.cs; ++r) {
-        const float2 v = peer_f2(own + i, r);
-        const float d = v.x - mu;
-        q += fmaf((float)((g.S * (r + 1) / g.cs - g.S * r / g.cs) * g.P) * d, d, v.y);
-      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < g.cs) {
+          const float d = v[r].x - mu;
+          q += fmaf(count(r) * d, d, v[r].y);
+        }
     } else {
       mu = own[i].x;
       q = own[i].y;
@@ -588,7 +734,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
     T* out = y + ((int64_t)p.n * g.S + p.r0 + p.lr) * ldy + p.c0 + p.lv * E;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (p.r0 + p.lr + (int64_t)k * p.rl >= p.r1) break;
+      if (p.r0 + p.lr + k * p.rl >= p.r1) break;
       float2 f[H];
       unpack2<T>(raw[k], f);
 #pragma unroll
@@ -644,7 +790,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 2 ? 2 : 1)
     for (int e = 0; e < H; ++e) A[e] = B[e] = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (p.r0 + p.lr + (int64_t)k * p.rl >= p.r1) break;
+      if (p.r0 + p.lr + k * p.rl >= p.r1) break;
       float2 f[H], d[H];
       unpack2<T>(raw[k], f);
       unpack2<T>(rawd[k], d);
@@ -654,7 +800,9 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 2 ? 2 : 1)
         const float2 gg = EPI == EPI_NONE ? d[e] : mul2(d[e], act_grad_pair<EPI, FAST>(fma2(xh, wf[e], bf[e])));
         A[e] = add2(A[e], gg);
         B[e] = fma2(gg, xh, B[e]);
+        if constexpr (sizeof(T) == 4) f[e] = xh, d[e] = gg;
       }
+      if constexpr (sizeof(T) == 4) raw[k] = pack2<T>(f), rawd[k] = pack2<T>(d);  // as they are needed below
     }
 #pragma unroll
     for (int e = 0; e < H; ++e) {
@@ -682,7 +830,11 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 2 ? 2 : 1)
   for (int c = threadIdx.x; c < p.nch; c += kResThreads) {
     float2 t = make_float2(0.0f, 0.0f);
     if (g.cs > 1) {
-      for (int r = 0; r < g.cs; ++r) t = add2(t, peer_f2(own + c, r));
+      float2 v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) v[r] = r < g.cs ? peer_f2(own + c, r) : make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) t = add2(t, v[r]);
     } else {
       t = own[c];
     }
@@ -718,14 +870,17 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 2 ? 2 : 1)
     T* out = dx + ((int64_t)p.n * g.S + p.r0 + p.lr) * lddx + p.c0 + p.lv * E;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (p.r0 + p.lr + (int64_t)k * p.rl >= p.r1) break;
+      if (p.r0 + p.lr + k * p.rl >= p.r1) break;
       float2 f[H], d[H];
       unpack2<T>(raw[k], f);
       unpack2<T>(rawd[k], d);
 #pragma unroll
       for (int e = 0; e < H; ++e) {
-        const float2 xh = mul2(add2(f[e], mu[e]), s[e]);
-        const float2 gg = EPI == EPI_NONE ? d[e] : mul2(d[e], act_grad_pair<EPI, FAST>(fma2(xh, wf[e], bf[e])));
+        float2 xh = f[e], gg = d[e];
+        if constexpr (sizeof(T) == 2) {
+          xh = mul2(add2(f[e], mu[e]), s[e]);
+          if constexpr (EPI != EPI_NONE) gg = mul2(d[e], act_grad_pair<EPI, FAST>(fma2(xh, wf[e], bf[e])));
+        }
         f[e] = mul2(s[e], fma2(xh, m2[e], fma2(gg, wf[e], m1[e])));
       }
       st_stream(out + (int64_t)k * p.rl * lddx, pack2<T>(f));
@@ -752,14 +907,22 @@ GnShape plan(int64_t N, int64_t S, int64_t C, int64_t G, int es) {
   g.tv = (nvec + g.tiles - 1) / g.tiles;
   g.rl = kThreads / g.tv;
   const int sms = sm_count() > 0 ? sm_count() : 148;
-  // about eight blocks per SM over the whole tensor, a slab no shorter than one batch per thread
-  int64_t chunks = (8 * (int64_t)sms + N * g.tiles - 1) / (N * g.tiles);
+  // about four blocks per SM over the whole tensor, a slab no shorter than one batch per thread
+  int64_t chunks = (4 * (int64_t)sms + N * g.tiles - 1) / (N * g.tiles);
   const int64_t most = (S + (int64_t)g.rl * kBatch - 1) / ((int64_t)g.rl * kBatch);
   if (chunks > most) chunks = most;
   if (chunks < 1) chunks = 1;
   g.rows = (S + chunks - 1) / chunks;
   g.chunks = (int)((S + g.rows - 1) / g.rows);
   return g;
+}
+
+// Images that the two passes take together (`bytes`: what the first pass reads of one): the second pass reads
+// them again, from L2 (126 MB) while they and what else passes through leave them there.
+int64_t images_at_once(int64_t N, int64_t bytes) {
+  constexpr int64_t kL2 = 64 << 20;
+  const int64_t n = bytes > 0 ? kL2 / bytes : N;
+  return n < 1 ? 1 : n < N ? n : N;
 }
 
 size_t up16(size_t v) { return (v + 15) / 16 * 16; }
@@ -783,10 +946,20 @@ void* pick_bwd(int epi) {
                                  : (void*)gn_bwd_apply_kernel<T, EPI_NONE>;
 }
 
-gn_status launch(void* kern, int64_t blocks, void** args, cudaStream_t s) {
+gn_status launch(void* kern, int64_t blocks, void** args, cudaStream_t s, bool waits) {
   if (blocks > INT32_MAX) return GN_ERR_SHAPE;
   if (!kernel_attrs(kern, 0)) return GN_ERR_CUDA;
-  if (cudaLaunchKernel(kern, dim3((unsigned)blocks), dim3(kThreads), args, 0, s) != cudaSuccess) return GN_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  // a kernel that waits for the one before it on the device (pdl_wait) may be launched while that one ends
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = GN_PDL;
+  cfg.attrs = attr;
+  cfg.numAttrs = waits ? 1 : 0;
+  if (cudaLaunchKernelExC(&cfg, kern, args) != cudaSuccess) return GN_ERR_CUDA;
   count_launches(1);
   return launch_status();
 }
@@ -822,6 +995,8 @@ Bundle plan_resident(int64_t N, int64_t S, int64_t C, int64_t G, int es, int mos
   while (v < need) v *= 2;
   *vpt = v;
   g.cs = cs;
+  g.rows = (int)((S + cs - 1) / cs);
+  while (g.lp < 5 && (1 << g.lp) < g.P) ++g.lp;
   return g;
 }
 
@@ -887,8 +1062,9 @@ extern "C" size_t gn_groupnorm_fwd_workspace(int64_t N, int64_t S, int64_t C, in
   if (!dt_ok(dt) || !shape_ok(N, S, C, G) || N == 0 || S == 0) return 0;
   int vpt = 0;
   if (plan_resident(N, S, C, G, (int)dt_size(dt), kFwdMost, &vpt).cs) return 0;
-  const GnShape g = plan(N, S, C, G, (int)dt_size(dt));
-  return up16((size_t)N * g.G * 8) + (size_t)N * g.chunks * g.C * 8;
+  const int64_t nb = images_at_once(N, S * C * (int64_t)dt_size(dt));
+  const GnShape g = plan(nb, S, C, G, (int)dt_size(dt));
+  return up16((size_t)N * g.G * 8) + (size_t)nb * g.chunks * g.C * 8;
 }
 
 extern "C" gn_status gn_groupnorm_fwd(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
@@ -911,31 +1087,38 @@ extern "C" gn_status gn_groupnorm_fwd(const void* x, const void* w, const void* 
   }
   if (!ws || ws_bytes < gn_groupnorm_fwd_workspace(N, S, C, G, dt)) return GN_ERR_WORKSPACE;
   if (!aligned16(ws)) return GN_ERR_ALIGN;
-  GnShape g = plan(N, S, C, G, (int)es);
-  float2* stat = static_cast<float2*>(ws);
+  const int64_t nb = images_at_once(N, S * C * (int64_t)es);
+  GnShape g = plan(nb, S, C, G, (int)es);
   float2* part = reinterpret_cast<float2*>(static_cast<char*>(ws) + up16((size_t)N * g.G * 8));
-  const int64_t blocks = N * g.chunks * g.tiles;
-  {
-    void* args[] = {&x, &ld_x, &g, &part};
-    const gn_status st =
-        launch(dt == GN_BF16 ? (void*)gn_stats_kernel<__nv_bfloat16> : (void*)gn_stats_kernel<float>, blocks, args, s);
+  void* apply = dt == GN_BF16 ? pick_apply<__nv_bfloat16>(epi) : pick_apply<float>(epi);
+  for (int64_t n0 = 0; n0 < N; n0 += nb) {
+    const int64_t n = N - n0 < nb ? N - n0 : nb, blocks = n * g.chunks * g.tiles;
+    const char* xn = static_cast<const char*>(x) + n0 * S * ld_x * (int64_t)es;
+    char* yn = static_cast<char*>(y) + n0 * S * ld_y * (int64_t)es;
+    float2* stat = static_cast<float2*>(ws) + n0 * G;
+    float* mn = mean ? mean + n0 * G : nullptr;
+    float* rn = rstd ? rstd + n0 * G : nullptr;
+    void* args0[] = {&xn, &ld_x, &g, &part};
+    gn_status st = launch(dt == GN_BF16 ? (void*)gn_stats_kernel<__nv_bfloat16> : (void*)gn_stats_kernel<float>, blocks,
+                          args0, s, false);
+    if (st != GN_OK) return st;
+    void* args1[] = {&part, &g, &eps, &stat, &mn, &rn};
+    st = launch((void*)gn_stats_join_kernel, n * G, args1, s, true);
+    if (st != GN_OK) return st;
+    void* args2[] = {&xn, &ld_x, &w, &b, &stat, &g, &yn, &ld_y};
+    st = launch(apply, blocks, args2, s, true);
     if (st != GN_OK) return st;
   }
-  {
-    void* args[] = {&part, &g, &eps, &stat, &mean, &rstd};
-    const gn_status st = launch((void*)gn_stats_join_kernel, N * g.G, args, s);
-    if (st != GN_OK) return st;
-  }
-  void* args[] = {&x, &ld_x, &w, &b, &stat, &g, &y, &ld_y};
-  return launch(dt == GN_BF16 ? pick_apply<__nv_bfloat16>(epi) : pick_apply<float>(epi), blocks, args, s);
+  return GN_OK;
 }
 
 extern "C" size_t gn_groupnorm_bwd_workspace(int64_t N, int64_t S, int64_t C, int64_t G, gn_dtype dt) {
   if (!dt_ok(dt) || !shape_ok(N, S, C, G) || N == 0 || S == 0) return 0;
   int vpt = 0;
   if (plan_resident(N, S, C, G, (int)dt_size(dt), kBwdMost, &vpt).cs) return (size_t)N * C * 8;
-  const GnShape g = plan(N, S, C, G, (int)dt_size(dt));
-  return up16((size_t)N * g.G * 8) + (size_t)N * g.C * 8 + (size_t)N * g.chunks * g.C * 8;
+  const int64_t nb = images_at_once(N, 2 * S * C * (int64_t)dt_size(dt));
+  const GnShape g = plan(nb, S, C, G, (int)dt_size(dt));
+  return up16((size_t)N * g.G * 8) + (size_t)N * g.C * 8 + (size_t)nb * g.chunks * g.C * 8;
 }
 
 extern "C" gn_status gn_groupnorm_bwd(const void* x, const void* w, const void* b, const float* mean,
@@ -966,26 +1149,30 @@ extern "C" gn_status gn_groupnorm_bwd(const void* x, const void* w, const void* 
     if (st != GN_OK || !chan) return st;
     return launch_colsum(chan, N, 2 * C, C, dw, db, s);
   }
-  GnShape g = plan(N, S, C, G, (int)es);
-  float2* stat = static_cast<float2*>(ws);
+  const int64_t nb = images_at_once(N, 2 * S * C * (int64_t)es);
+  GnShape g = plan(nb, S, C, G, (int)es);
   float* chan = reinterpret_cast<float*>(static_cast<char*>(ws) + up16((size_t)N * g.G * 8));
   float2* part = reinterpret_cast<float2*>(chan + (size_t)N * g.C * 2);
-  const int64_t blocks = N * g.chunks * g.tiles;
-  gn_status st;
-  {
-    void* args[] = {&x, &ld_x, &dy, &ld_dy, &w, &b, &mean, &rstd, &g, &part};
-    st = launch(dt == GN_BF16 ? pick_sums<__nv_bfloat16>(epi) : pick_sums<float>(epi), blocks, args, s);
+  void* sums = dt == GN_BF16 ? pick_sums<__nv_bfloat16>(epi) : pick_sums<float>(epi);
+  void* join = dt == GN_BF16 ? (void*)gn_bwd_join_kernel<__nv_bfloat16> : (void*)gn_bwd_join_kernel<float>;
+  void* apply = dt == GN_BF16 ? pick_bwd<__nv_bfloat16>(epi) : pick_bwd<float>(epi);
+  for (int64_t n0 = 0; n0 < N; n0 += nb) {
+    const int64_t n = N - n0 < nb ? N - n0 : nb, blocks = n * g.chunks * g.tiles;
+    const char* xn = static_cast<const char*>(x) + n0 * S * ld_x * (int64_t)es;
+    const char* dyn = static_cast<const char*>(dy) + n0 * S * ld_dy * (int64_t)es;
+    char* dxn = static_cast<char*>(dx) + n0 * S * ld_dx * (int64_t)es;
+    float2* stat = static_cast<float2*>(ws) + n0 * G;
+    float* ch = chan + n0 * 2 * C;
+    const float* mn = mean + n0 * G;
+    const float* rn = rstd + n0 * G;
+    void* args0[] = {&xn, &ld_x, &dyn, &ld_dy, &w, &b, &mn, &rn, &g, &part};
+    gn_status st = launch(sums, blocks, args0, s, false);
     if (st != GN_OK) return st;
-  }
-  {
-    void* args[] = {&part, &w, &g, &chan, &stat};
-    st = launch(dt == GN_BF16 ? (void*)gn_bwd_join_kernel<__nv_bfloat16> : (void*)gn_bwd_join_kernel<float>, N * g.G,
-                args, s);
+    void* args1[] = {&part, &w, &g, &ch, &stat};
+    st = launch(join, n * G, args1, s, true);
     if (st != GN_OK) return st;
-  }
-  {
-    void* args[] = {&x, &ld_x, &dy, &ld_dy, &w, &b, &mean, &rstd, &stat, &g, &dx, &ld_dx};
-    st = launch(dt == GN_BF16 ? pick_bwd<__nv_bfloat16>(epi) : pick_bwd<float>(epi), blocks, args, s);
+    void* args2[] = {&xn, &ld_x, &dyn, &ld_dy, &w, &b, &mn, &rn, &stat, &g, &dxn, &ld_dx};
+    st = launch(apply, blocks, args2, s, true);
     if (st != GN_OK) return st;
   }
   return launch_colsum(chan, N, 2 * C, C, dw, db, s);
