@@ -16,7 +16,7 @@
 // group in a fixed order, and an elementwise pass. A thread keeps one 16-byte vector of channels and
 // walks down the positions, so its per-channel sums and parameters stay in registers and every warp
 // access covers whole runs of a row. The forward's sums are (mean, centred sum of squares) per
-// channel, batch by batch with Chan's update: no E[x^2] - E[x]^2 cancellation.
+// channel, taken around a value of the slab and joined with Chan's update: no E[x^2] - E[x]^2 cancellation.
 #include <type_traits>
 
 #include "act_pairs.cuh"
@@ -27,7 +27,10 @@ namespace gn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 8;  // positions a thread has in flight in the forward's sums; half of it elsewhere
+// Positions that a thread takes together; while it works on them the next ones are on their way (all warps
+// start together: without that they load together and compute together, each half of the time).
+constexpr int kBatch = 4;      // forward
+constexpr int kBwdBatch = 2;   // backward: of x and of dy
 
 struct GnShape {
   int64_t S;       // positions of an image
@@ -89,68 +92,88 @@ struct Place {
 // ---------------------------------------------------------------- forward: slab statistics
 // part[n][chunk][c] = (mean, centred sum of squares) of channel c over the slab.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) gn_stats_kernel(const T* __restrict__ x, int64_t ldx, GnShape g,
+__global__ void __launch_bounds__(kThreads, 2) gn_stats_kernel(const T* __restrict__ x, int64_t ldx, GnShape g,
                                                             float2* __restrict__ part) {
   constexpr int E = Vec<T>::N, H = E / 2;
   __shared__ float sm_mean[kThreads * E];
   __shared__ float sm_m2[kThreads * E];
   __shared__ float sm_cnt[kThreads];
   const Place p = Place::make<E>(g);
-  float2 mean2[H], m22[H];
+  // sums of x - K and (x - K)^2 per channel, K the thread's first value: mean = K + s1 / n, squares
+  // = s2 - s1^2 / n, which loses at most four bits while s1^2 / n <= 16 squares; where the first value is
+  // further off than that, a second walk takes them around the mean
+  float2 shift[H], s1[H], s2[H];
   float cnt = 0.0f;
-#pragma unroll
-  for (int e = 0; e < H; ++e) mean2[e] = m22[e] = make_float2(0.0f, 0.0f);
-  // B positions: their mean and centred squares per channel, merged with what there is (Chan)
-  auto merge = [&](const uint4* u, auto size) {
-    constexpr int B = decltype(size)::value;
-    const float tot = cnt + B, fr = B / tot, wt = cnt * fr;
-#pragma unroll
-    for (int e = 0; e < H; ++e) {
-      float2 f[B], t = make_float2(0.0f, 0.0f), q = t;
-#pragma unroll
-      for (int k = 0; k < B; ++k) {
-        float2 all[H];
-        unpack2<T>(u[k], all);
-        f[k] = all[e];
-        t = add2(t, f[k]);
-      }
-      const float2 bm = mul2(t, dup2(1.0f / B)), nm = mul2(t, dup2(-1.0f / B));
-#pragma unroll
-      for (int k = 0; k < B; ++k) {
-        const float2 d = add2(f[k], nm);
-        q = fma2(d, d, q);
-      }
-      const float2 dl = add2(bm, mul2(mean2[e], dup2(-1.0f)));
-      mean2[e] = fma2(dl, dup2(fr), mean2[e]);
-      m22[e] = add2(m22[e], fma2(mul2(dl, dl), dup2(wt), q));
-    }
-    cnt = tot;
-  };
-  if (p.active) {
-    const T* row = x + ((int64_t)p.n * g.S + p.r0 + p.lane_row) * ldx;
+  if (p.active && p.r0 + p.lane_row < p.r1) {
+    const T* first = x + ((int64_t)p.n * g.S + p.r0 + p.lane_row) * ldx;
     const int64_t step = (int64_t)g.rl * ldx;
-    int64_t left = (p.r1 - p.r0 - p.lane_row + g.rl - 1) / g.rl;  // positions of this thread
-    if (p.whole) {
-      for (; left >= kBatch; left -= kBatch, row += kBatch * step) {
-        uint4 u[kBatch];
+    const int64_t positions = (p.r1 - p.r0 - p.lane_row + g.rl - 1) / g.rl;
+    cnt = (float)positions;
+    float f0[E];
+    load_vec<T>(first, p.v, g.C, p.whole, f0);
+#pragma unroll
+    for (int e = 0; e < H; ++e) shift[e] = make_float2(-f0[2 * e], -f0[2 * e + 1]);
+    auto add = [&](const uint4& u) {
+      float2 f[H];
+      unpack2<T>(u, f);
+#pragma unroll
+      for (int e = 0; e < H; ++e) {
+        const float2 d = add2(f[e], shift[e]);
+        s1[e] = add2(s1[e], d);
+        s2[e] = fma2(d, d, s2[e]);
+      }
+    };
+    for (int round = 0; round < 2; ++round) {
+#pragma unroll
+      for (int e = 0; e < H; ++e) s1[e] = s2[e] = make_float2(0.0f, 0.0f);
+      const T* row = first;
+      int64_t left = positions;
+      if (p.whole && left >= kBatch) {
+        uint4 u[kBatch], next[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) u[k] = *reinterpret_cast<const uint4*>(row + k * step + p.v * E);
-        merge(u, std::integral_constant<int, kBatch>{});
+        for (; left >= kBatch; left -= kBatch) {
+          row += kBatch * step;
+          if (left >= 2 * kBatch) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) next[k] = *reinterpret_cast<const uint4*>(row + k * step + p.v * E);
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            add(u[k]);
+            u[k] = next[k];
+          }
+        }
       }
-    }
-    for (; left > 0; --left, row += step) {
-      float f[E];
-      load_vec<T>(row, p.v, g.C, p.whole, f);
-      const uint4 u = Vec<T>::pack(f);
-      merge(&u, std::integral_constant<int, 1>{});
+      for (; left > 0; --left, row += step) {
+        float f[E];
+        load_vec<T>(row, p.v, g.C, p.whole, f);
+        add(Vec<T>::pack(f));
+      }
+      bool again = false;
+#pragma unroll
+      for (int e = 0; e < H; ++e) {
+        const float ax = s1[e].x * s1[e].x / cnt, ay = s1[e].y * s1[e].y / cnt;
+        again |= ax > 16.0f * (s2[e].x - ax) || ay > 16.0f * (s2[e].y - ay);
+      }
+      if (!again || round) break;
+#pragma unroll
+      for (int e = 0; e < H; ++e) shift[e] = make_float2(shift[e].x - s1[e].x / cnt, shift[e].y - s1[e].y / cnt);
     }
   }
   float mean[E], m2[E];
 #pragma unroll
   for (int e = 0; e < H; ++e) {
-    mean[2 * e] = mean2[e].x, mean[2 * e + 1] = mean2[e].y;
-    m2[2 * e] = m22[e].x, m2[2 * e + 1] = m22[e].y;
+    const bool any = cnt > 0.0f;
+    const float2 d = any ? make_float2(s1[e].x / cnt, s1[e].y / cnt) : make_float2(0.0f, 0.0f);
+    mean[2 * e] = any ? d.x - shift[e].x : 0.0f;
+    mean[2 * e + 1] = any ? d.y - shift[e].y : 0.0f;
+    // (a comparison that lets NaN through)
+    const float qx = any ? fmaf(-s1[e].x, d.x, s2[e].x) : 0.0f, qy = any ? fmaf(-s1[e].y, d.y, s2[e].y) : 0.0f;
+    m2[2 * e] = qx < 0.0f ? 0.0f : qx;
+    m2[2 * e + 1] = qy < 0.0f ? 0.0f : qy;
   }
+  pdl_launch_dependents();
 #pragma unroll
   for (int e = 0; e < E; ++e) sm_mean[threadIdx.x * E + e] = mean[e], sm_m2[threadIdx.x * E + e] = m2[e];
   sm_cnt[threadIdx.x] = cnt;
@@ -173,49 +196,59 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const T* __restrict_
   }
 }
 
-__device__ __forceinline__ float block_sum(float v, float* red) {  // kThreads threads, fixed order
+constexpr int kJoin = 1024;  // threads of the joins: the partial sums are few and a join waits on their latency
+
+__device__ __forceinline__ float block_sum(float v, float* red) {  // kJoin threads, fixed order
   v = group_sum<32>(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float t = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) t += red[i];
-  return t;
+  return group_sum<32>(red[threadIdx.x & 31]);
 }
 
 // one block per (image, group): joins the slabs and the group's channels. A thread takes every `parts`-th
-// slab of one channel (parts = kThreads / P, one where the group is wider).
-__global__ void __launch_bounds__(kThreads) gn_stats_join_kernel(const float2* __restrict__ part, GnShape g, float eps,
-                                                                 float2* __restrict__ stat, float* __restrict__ mean,
-                                                                 float* __restrict__ rstd) {
-  __shared__ float red[kThreads / 32];
-  pdl_wait();
+// slab of one channel (parts = kJoin / P, one where the group is wider), the first eight from registers in
+// the second round.
+__global__ void __launch_bounds__(kJoin) gn_stats_join_kernel(const float2* __restrict__ part, GnShape g, float eps,
+                                                              float2* __restrict__ stat, float* __restrict__ mean,
+                                                              float* __restrict__ rstd) {
+  constexpr int kHeld = 8;
+  __shared__ float red[kJoin / 32];
   const int n = blockIdx.x / g.G, gr = blockIdx.x % g.G;
   const float2* base = part + (int64_t)n * g.chunks * g.C + (int64_t)gr * g.P;
-  const int parts = g.P < kThreads ? kThreads / g.P : 1;
-  const int c0 = g.P < kThreads ? (int)threadIdx.x % g.P : (int)threadIdx.x;
-  const int k0 = g.P < kThreads ? (int)threadIdx.x / g.P : 0;
+  const int parts = g.P < kJoin ? kJoin / g.P : 1;
+  const int c0 = g.P < kJoin ? (int)threadIdx.x % g.P : (int)threadIdx.x;
+  const int k0 = g.P < kJoin ? (int)threadIdx.x / g.P : 0;
   auto count = [&](int k) {
     const int64_t r0 = (int64_t)k * g.rows;
     return (float)(g.S - r0 < g.rows ? g.S - r0 : g.rows);
   };
-  float t = 0.0f;
-  if (k0 < parts)
-    for (int c = c0; c < g.P; c += kThreads)
+  const bool mine = k0 < parts;
+  pdl_launch_dependents();
+  pdl_wait();
+  float2 v[kHeld];
+  float t = 0.0f, q = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int k = k0 + i * parts;
+    v[i] = mine && c0 < g.P && k < g.chunks ? base[(int64_t)k * g.C + c0] : make_float2(0.0f, 0.0f);
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (k0 + i * parts < g.chunks) t = fmaf(count(k0 + i * parts), v[i].x, t);
+  auto rest = [&](auto f) {  // what is not held in v
+    if (mine)
+      for (int c = c0; c < g.P; c += kJoin)
 #pragma unroll 4
-      for (int k = k0; k < g.chunks; k += parts) t = fmaf(count(k), base[(int64_t)k * g.C + c].x, t);
+        for (int k = k0 + (c == c0 ? kHeld * parts : 0); k < g.chunks; k += parts) f(count(k), base[(int64_t)k * g.C + c]);
+  };
+  rest([&](float n_, float2 u) { t = fmaf(n_, u.x, t); });
   const float total = (float)((double)g.S * g.P);
   const float mu = block_sum(t, red) / total;
-  float q = 0.0f;
-  if (k0 < parts)
-    for (int c = c0; c < g.P; c += kThreads)
-#pragma unroll 4
-      for (int k = k0; k < g.chunks; k += parts) {
-        const float2 v = base[(int64_t)k * g.C + c];
-        const float d = v.x - mu;
-        q += fmaf(count(k) * d, d, v.y);
-      }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (mine && c0 < g.P && k0 + i * parts < g.chunks) q += fmaf(count(k0 + i * parts) * (v[i].x - mu), v[i].x - mu, v[i].y);
+  rest([&](float n_, float2 u) { q += fmaf(n_ * (u.x - mu), u.x - mu, u.y); });
   const float var = block_sum(q, red) / total;
   if (threadIdx.x == 0) {
     const float s = 1.0f / sqrtf(var + eps);
@@ -227,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) gn_stats_join_kernel(const float2* _
 
 // ---------------------------------------------------------------- forward: the elementwise pass
 template <typename T, int EPI>
-__global__ void __launch_bounds__(kThreads) gn_apply_kernel(const T* x, int64_t ldx, const T* __restrict__ w,
+__global__ void __launch_bounds__(kThreads, 2) gn_apply_kernel(const T* x, int64_t ldx, const T* __restrict__ w,
                                                             const T* __restrict__ b, const float2* __restrict__ stat,
                                                             GnShape g, T* y, int64_t ldy) {
   constexpr int E = Vec<T>::N;
@@ -265,15 +298,25 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(const T* x, int64_t 
     for (int e = 0; e < E / 2; ++e) f[e] = act_pair<EPI, FAST>(fma2(add2(f[e], nmu[e]), a2[e], sh2[e]));
     return pack2<T>(f);
   };
-  if (p.whole) {
-    constexpr int B = kBatch / 2;
-    for (; left >= B; left -= B) {
-      uint4 u[B];
+  if (p.whole && left >= kBatch) {
+    const T* src = x + (img + p.r0 + p.lane_row + (left - 1) * g.rl) * ldx + p.v * E;
+    T* dst = y + (img + p.r0 + p.lane_row + (left - 1) * g.rl) * ldy + p.v * E;
+    const int64_t sx = (int64_t)g.rl * ldx, sy = (int64_t)g.rl * ldy;
+    uint4 u[kBatch], next[kBatch];
 #pragma unroll
-      for (int k = 0; k < B; ++k)
-        u[k] = ld_stream(x + (img + p.r0 + p.lane_row + (left - 1 - k) * g.rl) * ldx + p.v * E);
+    for (int k = 0; k < kBatch; ++k) u[k] = ld_stream(src - k * sx);
+    for (; left >= kBatch; left -= kBatch) {
+      src -= kBatch * sx;
+      if (left >= 2 * kBatch) {
 #pragma unroll
-      for (int k = 0; k < B; ++k) st_stream(y + (img + p.r0 + p.lane_row + (left - 1 - k) * g.rl) * ldy + p.v * E, one(u[k]));
+        for (int k = 0; k < kBatch; ++k) next[k] = ld_stream(src - k * sx);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        st_stream(dst - k * sy, one(u[k]));
+        u[k] = next[k];
+      }
+      dst -= kBatch * sy;
     }
   }
   for (; left > 0; --left) {
@@ -288,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(const T* x, int64_t 
 // ---------------------------------------------------------------- backward
 // part[n][chunk][c] = (A_c, B_c) = (sum g, sum g xhat) of channel c over the slab
 template <typename T, int EPI>
-__global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const T* __restrict__ x, int64_t ldx,
+__global__ void __launch_bounds__(kThreads, 2) gn_bwd_sums_kernel(const T* __restrict__ x, int64_t ldx,
                                                                const T* __restrict__ dy, int64_t lddy,
                                                                const T* __restrict__ w, const T* __restrict__ b,
                                                                const float* __restrict__ mean,
@@ -337,17 +380,31 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const T* __restri
     };
     const int64_t row0 = (int64_t)p.n * g.S + p.r0 + p.lane_row;
     int64_t left = (p.r1 - p.r0 - p.lane_row + g.rl - 1) / g.rl, r = row0;
-    if (p.whole) {
-      constexpr int B = kBatch / 2;
-      for (; left >= B; left -= B, r += B * g.rl) {
-        uint4 ux[B], ud[B];
+    if (p.whole && left >= kBwdBatch) {
+      const T* px = x + r * ldx + p.v * E;
+      const T* pd = dy + r * lddy + p.v * E;
+      const int64_t sx = (int64_t)g.rl * ldx, sd = (int64_t)g.rl * lddy;
+      uint4 ux[kBwdBatch], ud[kBwdBatch], nx[kBwdBatch], nd[kBwdBatch];
 #pragma unroll
-        for (int k = 0; k < B; ++k) {
-          ux[k] = *reinterpret_cast<const uint4*>(x + (r + k * g.rl) * ldx + p.v * E);
-          ud[k] = *reinterpret_cast<const uint4*>(dy + (r + k * g.rl) * lddy + p.v * E);
+      for (int k = 0; k < kBwdBatch; ++k) {
+        ux[k] = *reinterpret_cast<const uint4*>(px + k * sx);
+        ud[k] = *reinterpret_cast<const uint4*>(pd + k * sd);
+      }
+      for (; left >= kBwdBatch; left -= kBwdBatch, r += kBwdBatch * g.rl) {
+        px += kBwdBatch * sx;
+        pd += kBwdBatch * sd;
+        if (left >= 2 * kBwdBatch) {
+#pragma unroll
+          for (int k = 0; k < kBwdBatch; ++k) {
+            nx[k] = *reinterpret_cast<const uint4*>(px + k * sx);
+            nd[k] = *reinterpret_cast<const uint4*>(pd + k * sd);
+          }
         }
 #pragma unroll
-        for (int k = 0; k < B; ++k) one(ux[k], ud[k]);
+        for (int k = 0; k < kBwdBatch; ++k) {
+          one(ux[k], ud[k]);
+          ux[k] = nx[k], ud[k] = nd[k];
+        }
       }
     }
     for (; left > 0; --left, r += g.rl) {
@@ -362,6 +419,7 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const T* __restri
     A[2 * e] = A2[e].x, A[2 * e + 1] = A2[e].y;
     B[2 * e] = B2[e].x, B[2 * e + 1] = B2[e].y;
   }
+  pdl_launch_dependents();
 #pragma unroll
   for (int e = 0; e < E; ++e) sm_a[threadIdx.x * E + e] = A[e], sm_b[threadIdx.x * E + e] = B[e];
   __syncthreads();
@@ -380,22 +438,23 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const T* __restri
 // one block per (image, group): chan[n][0..C) = B_c, chan[n][C..2C) = A_c (the column sums over the
 // images are then dw and db), stat[n][group] = (m1, m2)
 template <typename T>
-__global__ void __launch_bounds__(kThreads) gn_bwd_join_kernel(const float2* __restrict__ part,
+__global__ void __launch_bounds__(kJoin) gn_bwd_join_kernel(const float2* __restrict__ part,
                                                                const T* __restrict__ w, GnShape g,
                                                                float* __restrict__ chan, float2* __restrict__ stat) {
-  __shared__ float red[kThreads / 32];
-  __shared__ float2 sums[kThreads];
+  __shared__ float red[kJoin / 32];
+  __shared__ float2 sums[kJoin];
+  pdl_launch_dependents();
   pdl_wait();
   const int n = blockIdx.x / g.G, gr = blockIdx.x % g.G;
   float m1 = 0.0f, m2 = 0.0f;
-  const int parts = g.P < kThreads ? kThreads / g.P : 1;
-  for (int b0 = 0; b0 < g.P; b0 += kThreads) {  // a thread: every `parts`-th slab of one channel
-    const int j = g.P < kThreads ? (int)threadIdx.x % g.P : b0 + (int)threadIdx.x;
-    const int k0 = g.P < kThreads ? (int)threadIdx.x / g.P : 0;
+  const int parts = g.P < kJoin ? kJoin / g.P : 1;
+  for (int b0 = 0; b0 < g.P; b0 += kJoin) {  // a thread: every `parts`-th slab of one channel
+    const int j = g.P < kJoin ? (int)threadIdx.x % g.P : b0 + (int)threadIdx.x;
+    const int k0 = g.P < kJoin ? (int)threadIdx.x / g.P : 0;
     float2 t = make_float2(0.0f, 0.0f);
     if (j < g.P && k0 < parts) {
       const float2* src = part + (int64_t)n * g.chunks * g.C + gr * g.P + j;
-#pragma unroll 4
+#pragma unroll 8
       for (int k = k0; k < g.chunks; k += parts) t = add2(t, src[(int64_t)k * g.C]);
     }
     sums[threadIdx.x] = t;
@@ -418,7 +477,7 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_join_kernel(const float2* __r
 }
 
 template <typename T, int EPI>
-__global__ void __launch_bounds__(kThreads) gn_bwd_apply_kernel(const T* __restrict__ x, int64_t ldx, const T* dy,
+__global__ void __launch_bounds__(kThreads, 2) gn_bwd_apply_kernel(const T* __restrict__ x, int64_t ldx, const T* dy,
                                                                 int64_t lddy, const T* __restrict__ w,
                                                                 const T* __restrict__ b, const float* __restrict__ mean,
                                                                 const float* __restrict__ rstd,
@@ -468,17 +527,27 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_apply_kernel(const T* __restr
   // the slab from its end: what the sums read last is still in L2
   const int64_t row0 = (int64_t)p.n * g.S + p.r0 + p.lane_row;
   int64_t left = (p.r1 - p.r0 - p.lane_row + g.rl - 1) / g.rl;
-  if (p.whole) {
-    constexpr int B = kBatch / 4;
-    for (; left >= B; left -= B) {
-      uint4 ux[B], ud[B];
+  if (p.whole && left >= kBwdBatch) {
+    const T* px = x + (row0 + (left - 1) * g.rl) * ldx + p.v * E;
+    const T* pd = dy + (row0 + (left - 1) * g.rl) * lddy + p.v * E;
+    T* out = dx + (row0 + (left - 1) * g.rl) * lddx + p.v * E;
+    const int64_t sx = (int64_t)g.rl * ldx, sd = (int64_t)g.rl * lddy, so = (int64_t)g.rl * lddx;
+    uint4 ux[kBwdBatch], ud[kBwdBatch], nx[kBwdBatch], nd[kBwdBatch];
 #pragma unroll
-      for (int k = 0; k < B; ++k) {
-        ux[k] = ld_stream(x + (row0 + (left - 1 - k) * g.rl) * ldx + p.v * E);
-        ud[k] = ld_stream(dy + (row0 + (left - 1 - k) * g.rl) * lddy + p.v * E);
+    for (int k = 0; k < kBwdBatch; ++k) ux[k] = ld_stream(px - k * sx), ud[k] = ld_stream(pd - k * sd);
+    for (; left >= kBwdBatch; left -= kBwdBatch) {
+      px -= kBwdBatch * sx;
+      pd -= kBwdBatch * sd;
+      if (left >= 2 * kBwdBatch) {
+#pragma unroll
+        for (int k = 0; k < kBwdBatch; ++k) nx[k] = ld_stream(px - k * sx), nd[k] = ld_stream(pd - k * sd);
       }
 #pragma unroll
-      for (int k = 0; k < B; ++k) st_stream(dx + (row0 + (left - 1 - k) * g.rl) * lddx + p.v * E, one(ux[k], ud[k]));
+      for (int k = 0; k < kBwdBatch; ++k) {
+        st_stream(out - k * so, one(ux[k], ud[k]));
+        ux[k] = nx[k], ud[k] = nd[k];
+      }
+      out -= kBwdBatch * so;
     }
   }
   for (; left > 0; --left) {
@@ -508,6 +577,7 @@ struct Bundle {
   int bundles;  // of an image
   int cs;       // blocks of a cluster
   int rows;     // positions of a block (the last ones may have fewer)
+  unsigned d_bv, d_w, d_p;  // for fdiv by bv, by the bundle's channels (whole vectors) and by P
   int lp;       // log2 of the lanes that take different channels of a group in a warp's sum
 };
 
@@ -538,6 +608,9 @@ __device__ __forceinline__ float2 peer_f2(const float2* p, int rank) {  // the s
   return v;
 }
 
+// n / d for n d < 2^32 by d's magic number ceil(2^32 / d) (0 for d = 1)
+__device__ __forceinline__ int fdiv(int n, unsigned m) { return m ? (int)__umulhi((unsigned)n, m) : n; }
+
 // what a thread of the resident kernels works on
 template <int E>
 struct ResPlace {
@@ -550,9 +623,9 @@ struct ResPlace {
     n = unit / g.bundles;
     c0 = (unit % g.bundles) * g.groups * g.P;
     nch = g.C - c0 < g.groups * g.P ? g.C - c0 : g.groups * g.P;
-    rl = kResThreads / g.bv;
-    lr = threadIdx.x / g.bv;
-    lv = threadIdx.x % g.bv;
+    rl = fdiv(kResThreads, g.d_bv);
+    lr = fdiv(threadIdx.x, g.d_bv);
+    lv = threadIdx.x - lr * g.bv;
     active = lr < rl && lv * E < nch;
     r0 = (int)(g.S < (int64_t)rank * g.rows ? g.S : rank * g.rows);
     r1 = (int)(g.S - r0 < g.rows ? g.S : r0 + g.rows);
@@ -574,7 +647,7 @@ __device__ __forceinline__ void res_load(uint4 (&raw)[VPT], const T* x, int64_t 
 // active). red: NQ x kResThreads x E floats. Returns the part sums in red2[q][part][W] (W = bv E, `parts`
 // parts), after a barrier; red and red2 may be the same memory (a barrier lies between).
 template <int E, int NQ>
-__device__ __forceinline__ int res_parts(const float (&v)[NQ][E], float* red, int W, int rl, bool in) {
+__device__ __forceinline__ int res_parts(const float (&v)[NQ][E], float* red, int W, unsigned d_w, int rl, bool in) {
   const int tid = threadIdx.x;
   if (in) {
 #pragma unroll
@@ -585,10 +658,11 @@ __device__ __forceinline__ int res_parts(const float (&v)[NQ][E], float* red, in
             make_float4(v[q][e], v[q][e + 1], v[q][e + 2], v[q][e + 3]);
   }
   __syncthreads();
-  const int parts = W < kResThreads ? kResThreads / W < rl ? kResThreads / W : rl : 1;
+  const int most = W < kResThreads ? fdiv(kResThreads, d_w) : 1, parts = most < rl ? most : rl;
+  const int row = W < kResThreads ? fdiv(tid, d_w) : 0, col = W < kResThreads ? tid - row * W : tid;
   // thread (part, channel) adds every parts-th position; blocks wider than kResThreads channels in rounds
   for (int c0 = 0; c0 < W; c0 += kResThreads) {
-    const int c = c0 + (W < kResThreads ? tid % W : tid), part = W < kResThreads ? tid / W : 0;
+    const int c = c0 + col, part = row;
     float t[NQ];
     const bool mine = part < parts && c < W;
 #pragma unroll
@@ -629,44 +703,53 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
   float* chan = reinterpret_cast<float*>(stat + g.groups);  // [3][W] mean, scale, shift of a channel
   const ResPlace<E> p(g);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ng = p.nch / g.P;
+  const int ng = fdiv(p.nch, g.d_p);
   uint4 raw[VPT];
   res_load<T, VPT>(raw, x, ldx, p, g.S);
   const float cnt = (float)(p.r1 - p.r0) * (float)g.P, inv_cnt = cnt > 0.0f ? 1.0f / cnt : 0.0f;
   {
     float s[1][E];
+    float2 t2[H];
 #pragma unroll
-    for (int e = 0; e < E; ++e) s[0][e] = 0.0f;
+    for (int e = 0; e < H; ++e) t2[e] = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      float f[E];
-      Vec<T>::unpack(raw[k], f);
+      float2 f[H];
+      unpack2<T>(raw[k], f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) s[0][e] += f[e];
+      for (int e = 0; e < H; ++e) t2[e] = add2(t2[e], f[e]);
     }
-    const int parts = res_parts<E, 1>(s, red, W, p.rl, p.lr < p.rl);
+#pragma unroll
+    for (int e = 0; e < H; ++e) s[0][2 * e] = t2[e].x, s[0][2 * e + 1] = t2[e].y;
+    const int parts = res_parts<E, 1>(s, red, W, g.d_w, p.rl, p.lr < p.rl);
     for (int i = warp; i < ng; i += kResThreads / 32) {
       const float t = warp_sum_of(red, W, parts, i * g.P, g.P, g.lp, lane);
       if (lane == 0) own[i].x = t * inv_cnt;
     }
     __syncthreads();
     keep_packed(raw);
-    float mu[E];
+    float2 nmu[H];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      s[0][e] = 0.0f;
-      mu[e] = p.active ? own[(p.lv * E + e) / g.P].x : 0.0f;
+    for (int e = 0; e < H; ++e) {
+      t2[e] = make_float2(0.0f, 0.0f);
+      const int c = p.active ? p.lv * E + 2 * e : 0;
+      nmu[e] = make_float2(-own[fdiv(c, g.d_p)].x, -own[fdiv(c + 1, g.d_p)].x);
     }
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (p.r0 + p.lr + k * p.rl < p.r1) {
-        float f[E];
-        Vec<T>::unpack(raw[k], f);
+      if (p.active && p.r0 + p.lr + k * p.rl < p.r1) {
+        float2 f[H];
+        unpack2<T>(raw[k], f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) s[0][e] = fmaf(f[e] - mu[e], f[e] - mu[e], s[0][e]);
+        for (int e = 0; e < H; ++e) {
+          const float2 d = add2(f[e], nmu[e]);
+          t2[e] = fma2(d, d, t2[e]);
+        }
       }
     }
-    const int parts2 = res_parts<E, 1>(s, red, W, p.rl, p.lr < p.rl);
+#pragma unroll
+    for (int e = 0; e < H; ++e) s[0][2 * e] = t2[e].x, s[0][2 * e + 1] = t2[e].y;
+    const int parts2 = res_parts<E, 1>(s, red, W, g.d_w, p.rl, p.lr < p.rl);
     for (int i = warp; i < ng; i += kResThreads / 32) {
       const float t = warp_sum_of(red, W, parts2, i * g.P, g.P, g.lp, lane);
       if (lane == 0) own[i].y = t;
@@ -708,7 +791,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
     const float s = 1.0f / sqrtf(q / total + eps);
     stat[i] = make_float2(mu, s);
     if (p.rank == 0) {
-      const int64_t at = (int64_t)p.n * g.G + p.c0 / g.P + i;
+      const int64_t at = (int64_t)p.n * g.G + (blockIdx.x / g.cs % g.bundles) * g.groups + i;
       if (mean) mean[at] = mu;
       if (rstd) rstd[at] = s;
     }
@@ -716,7 +799,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
   if (g.cs > 1) cluster_arrive();  // this block has read its peers (they may leave once all have)
   __syncthreads();
   for (int c = threadIdx.x; c < p.nch; c += kResThreads) {
-    const float2 s = stat[c / g.P];
+    const float2 s = stat[fdiv(c, g.d_p)];
     chan[c] = s.x;
     chan[W + c] = s.y * ld_param(w, p.c0 + c, 1.0f);
     chan[2 * W + c] = ld_param(b, p.c0 + c, 0.0f);
@@ -734,12 +817,11 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 4 ? 2 : 1)
     T* out = y + ((int64_t)p.n * g.S + p.r0 + p.lr) * ldy + p.c0 + p.lv * E;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (p.r0 + p.lr + k * p.rl >= p.r1) break;
       float2 f[H];
       unpack2<T>(raw[k], f);
 #pragma unroll
       for (int e = 0; e < H; ++e) f[e] = act_pair<EPI, FAST>(fma2(add2(f[e], mu[e]), a[e], sh[e]));
-      st_stream(out + (int64_t)k * p.rl * ldy, pack2<T>(f));
+      if (p.r0 + p.lr + k * p.rl < p.r1) st_stream(out + (int64_t)k * p.rl * ldy, pack2<T>(f));
     }
   }
   if (g.cs > 1) cluster_wait();
@@ -762,12 +844,13 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 2 ? 2 : 1)
   float* chan = reinterpret_cast<float*>(stat + g.groups);             // [4][W] mean, rstd, w, b of a channel
   const ResPlace<E> p(g);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ng = p.nch / g.P;
+  const int ng = fdiv(p.nch, g.d_p);
   uint4 raw[VPT], rawd[VPT];
   res_load<T, VPT>(raw, x, ldx, p, g.S);
   res_load<T, VPT>(rawd, dy, lddy, p, g.S);
+  const int g0 = (blockIdx.x / g.cs % g.bundles) * g.groups;  // the bundle's first group
   for (int c = threadIdx.x; c < p.nch; c += kResThreads) {
-    const int64_t at = (int64_t)p.n * g.G + (p.c0 + c) / g.P;
+    const int64_t at = (int64_t)p.n * g.G + g0 + fdiv(c, g.d_p);
     chan[c] = mean[at];
     chan[W + c] = rstd[at];
     chan[2 * W + c] = ld_param(w, p.c0 + c, 1.0f);
@@ -789,8 +872,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 2 ? 2 : 1)
 #pragma unroll
     for (int e = 0; e < H; ++e) A[e] = B[e] = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      if (p.r0 + p.lr + k * p.rl >= p.r1) break;
+    for (int k = 0; k < VPT; ++k) {  // past the block's positions dy is 0 and adds nothing
       float2 f[H], d[H];
       unpack2<T>(raw[k], f);
       unpack2<T>(rawd[k], d);
@@ -812,7 +894,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 2 ? 2 : 1)
   }
   keep_packed(raw);
   keep_packed(rawd);
-  const int parts = res_parts<E, 2>(v, red, W, p.rl, p.lr < p.rl);
+  const int parts = res_parts<E, 2>(v, red, W, g.d_w, p.rl, p.lr < p.rl);
   for (int c = threadIdx.x; c < p.nch; c += kResThreads) {
     float ta = 0.0f, tb = 0.0f;
     for (int k = 0; k < parts; ++k) {
@@ -863,14 +945,13 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 2 ? 2 : 1)
     float2 m1[H], m2[H];
 #pragma unroll
     for (int e = 0; e < H; ++e) {
-      const float2 u = stat[(p.lv * E + 2 * e) / g.P], t = stat[(p.lv * E + 2 * e + 1) / g.P];
+      const float2 u = stat[fdiv(p.lv * E + 2 * e, g.d_p)], t = stat[fdiv(p.lv * E + 2 * e + 1, g.d_p)];
       m1[e] = make_float2(-u.x, -t.x);
       m2[e] = make_float2(-u.y, -t.y);
     }
     T* out = dx + ((int64_t)p.n * g.S + p.r0 + p.lr) * lddx + p.c0 + p.lv * E;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (p.r0 + p.lr + k * p.rl >= p.r1) break;
       float2 f[H], d[H];
       unpack2<T>(raw[k], f);
       unpack2<T>(rawd[k], d);
@@ -883,7 +964,7 @@ __global__ void __launch_bounds__(kResThreads, VPT <= 2 ? 2 : 1)
         }
         f[e] = mul2(s[e], fma2(xh, m2[e], fma2(gg, wf[e], m1[e])));
       }
-      st_stream(out + (int64_t)k * p.rl * lddx, pack2<T>(f));
+      if (p.r0 + p.lr + k * p.rl < p.r1) st_stream(out + (int64_t)k * p.rl * lddx, pack2<T>(f));
     }
   }
   if (g.cs > 1) cluster_wait();
@@ -907,12 +988,16 @@ GnShape plan(int64_t N, int64_t S, int64_t C, int64_t G, int es) {
   g.tv = (nvec + g.tiles - 1) / g.tiles;
   g.rl = kThreads / g.tv;
   const int sms = sm_count() > 0 ? sm_count() : 148;
-  // about four blocks per SM over the whole tensor, a slab no shorter than one batch per thread
-  int64_t chunks = (4 * (int64_t)sms + N * g.tiles - 1) / (N * g.tiles);
+  // the two blocks per SM that are resident at once, a slab no shorter than one batch per thread
+  int64_t chunks = 2 * (int64_t)sms / (N * g.tiles);
+  if (chunks < 1) chunks = 1;
   const int64_t most = (S + (int64_t)g.rl * kBatch - 1) / ((int64_t)g.rl * kBatch);
   if (chunks > most) chunks = most;
   if (chunks < 1) chunks = 1;
+  // in whole batches: what is left of one is read position by position, a memory latency each
+  const int64_t batch = (int64_t)g.rl * kBatch;
   g.rows = (S + chunks - 1) / chunks;
+  if (g.rows > batch) g.rows = (g.rows + batch - 1) / batch * batch;
   g.chunks = (int)((S + g.rows - 1) / g.rows);
   return g;
 }
@@ -946,12 +1031,12 @@ void* pick_bwd(int epi) {
                                  : (void*)gn_bwd_apply_kernel<T, EPI_NONE>;
 }
 
-gn_status launch(void* kern, int64_t blocks, void** args, cudaStream_t s, bool waits) {
+gn_status launch(void* kern, int64_t blocks, void** args, cudaStream_t s, bool waits, int threads = kThreads) {
   if (blocks > INT32_MAX) return GN_ERR_SHAPE;
   if (!kernel_attrs(kern, 0)) return GN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = s;
   // a kernel that waits for the one before it on the device (pdl_wait) may be launched while that one ends
   cudaLaunchAttribute attr[1];
@@ -981,7 +1066,7 @@ Bundle plan_resident(int64_t N, int64_t S, int64_t C, int64_t G, int es, int mos
   if (per > G) return g;
   int64_t bv = per * run / 16;
   auto fits = [&](int64_t v, int64_t cs) { return v <= kResThreads && (S + cs - 1) / cs <= (kResThreads / v) * (int64_t)most; };
-  if (!fits(bv, 8)) return g;
+  if (!fits(bv, 8) || (N * S * C * es > (4 << 20) && !fits(bv, 1))) return g;
   while (bv < 4 && per * 2 <= G && fits(bv * 2, 8)) per *= 2, bv *= 2;
   g.groups = per;
   g.bv = (int)bv;
@@ -991,11 +1076,13 @@ Bundle plan_resident(int64_t N, int64_t S, int64_t C, int64_t G, int es, int mos
   int cs = 1;
   while (cs < 8 && (!fits(bv, cs) || (units * cs < 2 * sms && (S + cs - 1) / cs > 2 * (kResThreads / bv)))) cs *= 2;
   const int64_t need = ((S + cs - 1) / cs + kResThreads / bv - 1) / (kResThreads / bv);
-  int v = 1;
-  while (v < need) v *= 2;
-  *vpt = v;
+  *vpt = need <= 2 ? (int)need : need <= 8 ? (int)(need + 1) / 2 * 2 : (int)(need + 3) / 4 * 4;
   g.cs = cs;
   g.rows = (int)((S + cs - 1) / cs);
+  auto magic = [](int64_t d) { return d > 1 ? (unsigned)(((1ull << 32) + d - 1) / d) : 0u; };
+  g.d_bv = magic(bv);
+  g.d_w = magic(bv * 16 / es);
+  g.d_p = magic(g.P);
   while (g.lp < 5 && (1 << g.lp) < g.P) ++g.lp;
   return g;
 }
@@ -1005,7 +1092,9 @@ void* pick_fwd_res(int vpt) {
   return vpt <= 1   ? (void*)gn_fwd_resident_kernel<T, EPI, 1>
          : vpt <= 2 ? (void*)gn_fwd_resident_kernel<T, EPI, 2>
          : vpt <= 4 ? (void*)gn_fwd_resident_kernel<T, EPI, 4>
+         : vpt <= 6 ? (void*)gn_fwd_resident_kernel<T, EPI, 6>
          : vpt <= 8 ? (void*)gn_fwd_resident_kernel<T, EPI, 8>
+         : vpt <= 12 ? (void*)gn_fwd_resident_kernel<T, EPI, 12>
                     : (void*)gn_fwd_resident_kernel<T, EPI, 16>;
 }
 template <typename T, int EPI>
@@ -1013,6 +1102,7 @@ void* pick_bwd_res(int vpt) {
   return vpt <= 1   ? (void*)gn_bwd_resident_kernel<T, EPI, 1>
          : vpt <= 2 ? (void*)gn_bwd_resident_kernel<T, EPI, 2>
          : vpt <= 4 ? (void*)gn_bwd_resident_kernel<T, EPI, 4>
+         : vpt <= 6 ? (void*)gn_bwd_resident_kernel<T, EPI, 6>
                     : (void*)gn_bwd_resident_kernel<T, EPI, 8>;
 }
 template <typename T>
@@ -1103,7 +1193,7 @@ extern "C" gn_status gn_groupnorm_fwd(const void* x, const void* w, const void* 
                           args0, s, false);
     if (st != GN_OK) return st;
     void* args1[] = {&part, &g, &eps, &stat, &mn, &rn};
-    st = launch((void*)gn_stats_join_kernel, n * G, args1, s, true);
+    st = launch((void*)gn_stats_join_kernel, n * G, args1, s, true, kJoin);
     if (st != GN_OK) return st;
     void* args2[] = {&xn, &ld_x, &w, &b, &stat, &g, &yn, &ld_y};
     st = launch(apply, blocks, args2, s, true);
@@ -1169,7 +1259,7 @@ extern "C" gn_status gn_groupnorm_bwd(const void* x, const void* w, const void* 
     gn_status st = launch(sums, blocks, args0, s, false);
     if (st != GN_OK) return st;
     void* args1[] = {&part, &w, &g, &ch, &stat};
-    st = launch(join, n * G, args1, s, true);
+    st = launch(join, n * G, args1, s, true, kJoin);
     if (st != GN_OK) return st;
     void* args2[] = {&xn, &ld_x, &dyn, &ld_dy, &w, &b, &mn, &rn, &stat, &g, &dxn, &ld_dx};
     st = launch(apply, blocks, args2, s, true);
