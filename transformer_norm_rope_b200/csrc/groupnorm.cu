@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_apply_kernel(const T* x, int64
     a2[e] = make_float2(a[2 * e], a[2 * e + 1]);
     sh2[e] = make_float2(sh[2 * e], sh[2 * e + 1]);
   }
-  // the slab from its end: what the sums read last is still in L2
+  // the slab from its end, which the sums read last: as much of it as L2 still holds is not read from HBM again
   const int64_t img = (int64_t)p.n * g.S;
   int64_t left = (p.r1 - p.r0 - p.lane_row + g.rl - 1) / g.rl;  // positions of this thread
   auto one = [&](const uint4& u) {
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_apply_kernel(const T* __re
     }
     return pack2<T>(f);
   };
-  // the slab from its end: what the sums read last is still in L2
+  // the slab from its end, which the sums read last: as much of it as L2 still holds is not read from HBM again
   const int64_t row0 = (int64_t)p.n * g.S + p.r0 + p.lane_row;
   int64_t left = (p.r1 - p.r0 - p.lane_row + g.rl - 1) / g.rl;
   if (p.whole && left >= kBwdBatch) {
@@ -1002,14 +1002,6 @@ GnShape plan(int64_t N, int64_t S, int64_t C, int64_t G, int es) {
   return g;
 }
 
-// Images that the two passes take together (`bytes`: what the first pass reads of one): the second pass reads
-// them again, from L2 (126 MB) while they and what else passes through leave them there.
-int64_t images_at_once(int64_t N, int64_t bytes) {
-  constexpr int64_t kL2 = 64 << 20;
-  const int64_t n = bytes > 0 ? kL2 / bytes : N;
-  return n < 1 ? 1 : n < N ? n : N;
-}
-
 size_t up16(size_t v) { return (v + 15) / 16 * 16; }
 
 template <typename T>
@@ -1068,10 +1060,14 @@ Bundle plan_resident(int64_t N, int64_t S, int64_t C, int64_t G, int es, int mos
   auto fits = [&](int64_t v, int64_t cs) { return v <= kResThreads && (S + cs - 1) / cs <= (kResThreads / v) * (int64_t)most; };
   if (!fits(bv, 8) || (N * S * C * es > (4 << 20) && !fits(bv, 1))) return g;
   while (bv < 4 && per * 2 <= G && fits(bv * 2, 8)) per *= 2, bv *= 2;
+  // many small images: wider bundles while there are blocks enough, so that a block's threads have work
+  const int sms = sm_count() > 0 ? sm_count() : 148;
+  while (per * 2 <= G && N * ((G + 2 * per - 1) / (2 * per)) >= 2 * sms && bv * 2 <= kResThreads &&
+         S <= (kResThreads / (bv * 2)) * 4)
+    per *= 2, bv *= 2;
   g.groups = per;
   g.bv = (int)bv;
   g.bundles = (int)((G + per - 1) / per);
-  const int sms = sm_count() > 0 ? sm_count() : 148;
   const int64_t units = N * g.bundles;
   int cs = 1;
   while (cs < 8 && (!fits(bv, cs) || (units * cs < 2 * sms && (S + cs - 1) / cs > 2 * (kResThreads / bv)))) cs *= 2;
@@ -1152,9 +1148,8 @@ extern "C" size_t gn_groupnorm_fwd_workspace(int64_t N, int64_t S, int64_t C, in
   if (!dt_ok(dt) || !shape_ok(N, S, C, G) || N == 0 || S == 0) return 0;
   int vpt = 0;
   if (plan_resident(N, S, C, G, (int)dt_size(dt), kFwdMost, &vpt).cs) return 0;
-  const int64_t nb = images_at_once(N, S * C * (int64_t)dt_size(dt));
-  const GnShape g = plan(nb, S, C, G, (int)dt_size(dt));
-  return up16((size_t)N * g.G * 8) + (size_t)nb * g.chunks * g.C * 8;
+  const GnShape g = plan(N, S, C, G, (int)dt_size(dt));
+  return up16((size_t)N * g.G * 8) + (size_t)N * g.chunks * g.C * 8;
 }
 
 extern "C" gn_status gn_groupnorm_fwd(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
@@ -1177,38 +1172,27 @@ extern "C" gn_status gn_groupnorm_fwd(const void* x, const void* w, const void* 
   }
   if (!ws || ws_bytes < gn_groupnorm_fwd_workspace(N, S, C, G, dt)) return GN_ERR_WORKSPACE;
   if (!aligned16(ws)) return GN_ERR_ALIGN;
-  const int64_t nb = images_at_once(N, S * C * (int64_t)es);
-  GnShape g = plan(nb, S, C, G, (int)es);
+  GnShape g = plan(N, S, C, G, (int)es);
+  float2* stat = static_cast<float2*>(ws);
   float2* part = reinterpret_cast<float2*>(static_cast<char*>(ws) + up16((size_t)N * g.G * 8));
-  void* apply = dt == GN_BF16 ? pick_apply<__nv_bfloat16>(epi) : pick_apply<float>(epi);
-  for (int64_t n0 = 0; n0 < N; n0 += nb) {
-    const int64_t n = N - n0 < nb ? N - n0 : nb, blocks = n * g.chunks * g.tiles;
-    const char* xn = static_cast<const char*>(x) + n0 * S * ld_x * (int64_t)es;
-    char* yn = static_cast<char*>(y) + n0 * S * ld_y * (int64_t)es;
-    float2* stat = static_cast<float2*>(ws) + n0 * G;
-    float* mn = mean ? mean + n0 * G : nullptr;
-    float* rn = rstd ? rstd + n0 * G : nullptr;
-    void* args0[] = {&xn, &ld_x, &g, &part};
-    gn_status st = launch(dt == GN_BF16 ? (void*)gn_stats_kernel<__nv_bfloat16> : (void*)gn_stats_kernel<float>, blocks,
-                          args0, s, false);
-    if (st != GN_OK) return st;
-    void* args1[] = {&part, &g, &eps, &stat, &mn, &rn};
-    st = launch((void*)gn_stats_join_kernel, n * G, args1, s, true, kJoin);
-    if (st != GN_OK) return st;
-    void* args2[] = {&xn, &ld_x, &w, &b, &stat, &g, &yn, &ld_y};
-    st = launch(apply, blocks, args2, s, true);
-    if (st != GN_OK) return st;
-  }
-  return GN_OK;
+  const int64_t blocks = N * g.chunks * g.tiles;
+  void* args0[] = {&x, &ld_x, &g, &part};
+  gn_status st = launch(dt == GN_BF16 ? (void*)gn_stats_kernel<__nv_bfloat16> : (void*)gn_stats_kernel<float>, blocks, args0,
+                        s, false);
+  if (st != GN_OK) return st;
+  void* args1[] = {&part, &g, &eps, &stat, &mean, &rstd};
+  st = launch((void*)gn_stats_join_kernel, N * G, args1, s, true, kJoin);
+  if (st != GN_OK) return st;
+  void* args2[] = {&x, &ld_x, &w, &b, &stat, &g, &y, &ld_y};
+  return launch(dt == GN_BF16 ? pick_apply<__nv_bfloat16>(epi) : pick_apply<float>(epi), blocks, args2, s, true);
 }
 
 extern "C" size_t gn_groupnorm_bwd_workspace(int64_t N, int64_t S, int64_t C, int64_t G, gn_dtype dt) {
   if (!dt_ok(dt) || !shape_ok(N, S, C, G) || N == 0 || S == 0) return 0;
   int vpt = 0;
   if (plan_resident(N, S, C, G, (int)dt_size(dt), kBwdMost, &vpt).cs) return (size_t)N * C * 8;
-  const int64_t nb = images_at_once(N, 2 * S * C * (int64_t)dt_size(dt));
-  const GnShape g = plan(nb, S, C, G, (int)dt_size(dt));
-  return up16((size_t)N * g.G * 8) + (size_t)N * g.C * 8 + (size_t)nb * g.chunks * g.C * 8;
+  const GnShape g = plan(N, S, C, G, (int)dt_size(dt));
+  return up16((size_t)N * g.G * 8) + (size_t)N * g.C * 8 + (size_t)N * g.chunks * g.C * 8;
 }
 
 extern "C" gn_status gn_groupnorm_bwd(const void* x, const void* w, const void* b, const float* mean,
@@ -1239,31 +1223,20 @@ extern "C" gn_status gn_groupnorm_bwd(const void* x, const void* w, const void* 
     if (st != GN_OK || !chan) return st;
     return launch_colsum(chan, N, 2 * C, C, dw, db, s);
   }
-  const int64_t nb = images_at_once(N, 2 * S * C * (int64_t)es);
-  GnShape g = plan(nb, S, C, G, (int)es);
+  GnShape g = plan(N, S, C, G, (int)es);
+  float2* stat = static_cast<float2*>(ws);
   float* chan = reinterpret_cast<float*>(static_cast<char*>(ws) + up16((size_t)N * g.G * 8));
   float2* part = reinterpret_cast<float2*>(chan + (size_t)N * g.C * 2);
-  void* sums = dt == GN_BF16 ? pick_sums<__nv_bfloat16>(epi) : pick_sums<float>(epi);
-  void* join = dt == GN_BF16 ? (void*)gn_bwd_join_kernel<__nv_bfloat16> : (void*)gn_bwd_join_kernel<float>;
-  void* apply = dt == GN_BF16 ? pick_bwd<__nv_bfloat16>(epi) : pick_bwd<float>(epi);
-  for (int64_t n0 = 0; n0 < N; n0 += nb) {
-    const int64_t n = N - n0 < nb ? N - n0 : nb, blocks = n * g.chunks * g.tiles;
-    const char* xn = static_cast<const char*>(x) + n0 * S * ld_x * (int64_t)es;
-    const char* dyn = static_cast<const char*>(dy) + n0 * S * ld_dy * (int64_t)es;
-    char* dxn = static_cast<char*>(dx) + n0 * S * ld_dx * (int64_t)es;
-    float2* stat = static_cast<float2*>(ws) + n0 * G;
-    float* ch = chan + n0 * 2 * C;
-    const float* mn = mean + n0 * G;
-    const float* rn = rstd + n0 * G;
-    void* args0[] = {&xn, &ld_x, &dyn, &ld_dy, &w, &b, &mn, &rn, &g, &part};
-    gn_status st = launch(sums, blocks, args0, s, false);
-    if (st != GN_OK) return st;
-    void* args1[] = {&part, &w, &g, &ch, &stat};
-    st = launch(join, n * G, args1, s, true, kJoin);
-    if (st != GN_OK) return st;
-    void* args2[] = {&xn, &ld_x, &dyn, &ld_dy, &w, &b, &mn, &rn, &stat, &g, &dxn, &ld_dx};
-    st = launch(apply, blocks, args2, s, true);
-    if (st != GN_OK) return st;
-  }
+  const int64_t blocks = N * g.chunks * g.tiles;
+  void* args0[] = {&x, &ld_x, &dy, &ld_dy, &w, &b, &mean, &rstd, &g, &part};
+  gn_status st = launch(dt == GN_BF16 ? pick_sums<__nv_bfloat16>(epi) : pick_sums<float>(epi), blocks, args0, s, false);
+  if (st != GN_OK) return st;
+  void* args1[] = {&part, &w, &g, &chan, &stat};
+  st = launch(dt == GN_BF16 ? (void*)gn_bwd_join_kernel<__nv_bfloat16> : (void*)gn_bwd_join_kernel<float>, N * G, args1, s,
+              true, kJoin);
+  if (st != GN_OK) return st;
+  void* args2[] = {&x, &ld_x, &dy, &ld_dy, &w, &b, &mean, &rstd, &stat, &g, &dx, &ld_dx};
+  st = launch(dt == GN_BF16 ? pick_bwd<__nv_bfloat16>(epi) : pick_bwd<float>(epi), blocks, args2, s, true);
+  if (st != GN_OK) return st;
   return launch_colsum(chan, N, 2 * C, C, dw, db, s);
 }
