@@ -501,23 +501,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // columns m. The totals go to shared memory, [m][n] fp32; after a cluster barrier CTA r adds the CS
 // copies of its share of the rows m in rank order and writes it.
 constexpr int kSplitThreads = 192;
+constexpr int kTotLd = 132;  // floats between the rows of the totals: conflict-free for both who write and who read them
 template <int MT>
 struct Split {
   static constexpr uint32_t Stage = kTileBytes + MT * kBlk;
-  static constexpr int Stages = MT == 16 ? 6 : MT == 32 ? 5 : MT == 64 ? 4 : 3;  // two CTAs per SM
+  static constexpr int Stages = MT == 16 ? 6 : MT == 32 ? 5 : MT == 64 ? 4 : 6;
+  static constexpr int PerSm = MT == 128 ? 1 : 2;  // CTAs: 128 totals a thread leave room for one
   static constexpr uint32_t TmemCols = 2 * MT;
   static constexpr size_t Smem = 1024 + (size_t)Stages * Stage + 256 + 2 * MT * 4;
-  static_assert((size_t)Stages * Stage >= (size_t)MT * 128 * 4, "the totals reuse the stages");
+  static_assert((size_t)Stages * Stage >= (size_t)MT * kTotLd * 4, "the totals reuse the stages");
 };
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
 
+// Rows i0 .. i1 of the output tile: a warp adds the cs copies of its rows in rank order, four columns a lane. U rows
+// at a time, all their copies under way together (a read from another SM takes hundreds of cycles).
+template <int CS, int U, int EPI, bool F32>
+__device__ __forceinline__ void add_totals(const Fp8Args& a, const float* total, int cs, int n0, int m0, int i0, int i1,
+                                           int warp, int lane) {
+  const int n = n0 + 4 * lane;
+  uint32_t peer[CS];
+#pragma unroll
+  for (int j = 0; j < CS; ++j) peer[j] = cluster_addr(total, j < cs ? (uint32_t)j : 0u) + 16u * (uint32_t)lane;
+  float d[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d[e] = a.d && n + e < a.N ? __ldg(a.d + n + e) : 0.0f;
+  if (i1 > a.M - m0) i1 = a.M - m0;
+  for (int i = i0 + warp; i < i1; i += 4 * U) {
+    float4 v[U][CS];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < CS; ++j)
+        if (j < cs && i + 4 * u < i1) v[u][j] = ld_cluster(peer[j] + (uint32_t)(i + 4 * u) * (4u * kTotLd));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + 4 * u >= i1) break;
+      float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < CS; ++j)
+        if (j < cs) z[0] += v[u][j].x, z[1] += v[u][j].y, z[2] += v[u][j].z, z[3] += v[u][j].w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[e] = f8_act<EPI>(z[e] + d[e]);
+      const int64_t at = (int64_t)(m0 + i + 4 * u) * a.ldy + n;
+      if constexpr (F32) {
+        float* p = static_cast<float*>(a.y) + at;
+        if (n + 4 <= a.N) {
+          float4 o = make_float4(z[0], z[1], z[2], z[3]);
+          if (a.accumulate) {
+            const float4 c = *reinterpret_cast<const float4*>(p);
+            o.x += c.x, o.y += c.y, o.z += c.z, o.w += c.w;
+          }
+          *reinterpret_cast<float4*>(p) = o;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) p[e] = a.accumulate ? p[e] + z[e] : z[e];
+        }
+      } else {
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.y) + at;
+        if (n + 4 <= a.N) {
+          *reinterpret_cast<uint2*>(p) = make_uint2(Vec<__nv_bfloat16>::join(z[0], z[1]), Vec<__nv_bfloat16>::join(z[2], z[3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) p[e] = __float2bfloat16_rn(z[e]);
+        }
+      }
+    }
+  }
+}
+
 template <int MT, int EPI, bool F32>
-__global__ void __launch_bounds__(kSplitThreads, 2)
+__global__ void __launch_bounds__(kSplitThreads, Split<MT>::PerSm)
     linear_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                             const Fp8Args a, int cs) {
   using SP = Split<MT>;
@@ -531,7 +591,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(acce + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   float* sa_col = reinterpret_cast<float*>(smem + kStages * SP::Stage + 256);  // [2][MT]
-  float* total = reinterpret_cast<float*>(smem);                              // [MT][128]
+  float* total = reinterpret_cast<float*>(smem);                              // [MT][kTotLd]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int n0 = (int)(blockIdx.x / cs) * 128, m0 = (int)blockIdx.y * MT;
@@ -557,7 +617,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tslot;
   bool ok = true;
-  float acc[MT];
+  constexpr bool FRAG = MT >= 32;
+  float2 acc[MT / 2];
 
   if (warp == 0) {
     if (lane == 0) {
@@ -605,35 +666,75 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const int q = warp & 3;
     const int ct = threadIdx.x - 64;   // 0..127
     const int n = n0 + 32 * q + lane;  // this thread's column of y
-    const float* sb = a.sb + (int64_t)((n < a.N ? n : a.N - 1) >> a.b_shift) * a.ldsb;
+    // FRAG: four columns of y (lane / 4 + 8 i of the warp's 32) and MT / 4 rows a thread, so that it reads as
+    // many of A's scales; with one column and MT rows a thread those reads alone, 512 bytes to a warp and
+    // value, took the shared memory 512 cycles a block at MT = 128
+    constexpr int kCols = FRAG ? 4 : 1;
+    const int nq = n0 + 32 * q;
+    const float* sb[kCols];
+    float sb_next[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const int c = FRAG ? nq + (lane >> 2) + 8 * i : n;
+      sb[i] = a.sb + (int64_t)((c < a.N ? c : a.N - 1) >> a.b_shift) * a.ldsb;
+      sb_next[i] = kb0 < kb1 ? __ldg(sb[i] + kb0) : 0.0f;
+    }
     const float* sa = a.sa + (int64_t)(m0 + ct < a.M ? m0 + ct : a.M - 1) * a.ldsa;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = 0.0f;
-    float sb_next = kb0 < kb1 ? __ldg(sb + kb0) : 0.0f, sa_next = kb0 < kb1 && ct < MT ? __ldg(sa + kb0) : 0.0f;
+    for (int i = 0; i < MT / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+    float sa_next = kb0 < kb1 && ct < MT ? __ldg(sa + kb0) : 0.0f;
     for (int kb = kb0; kb < kb1; ++kb) {
       const int i = kb - kb0, buf = i & 1;
-      const float sbv = sb_next;
+      float sbv[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) sbv[c] = sb_next[c];
       if (ct < MT) sa_col[buf * MT + ct] = sa_next;  // last read before the barrier of the block before
       asm volatile("bar.sync 1, 128;" ::: "memory");
       if (kb + 1 < kb1) {
-        sb_next = __ldg(sb + kb + 1);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) sb_next[c] = __ldg(sb[c] + kb + 1);
         if (ct < MT) sa_next = __ldg(sa + kb + 1);
       }
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&accf[buf], (uint32_t)(i >> 1) & 1u, a.err)) && !*abort_flag;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&accf[buf], (uint32_t)(i >> 1) & 1u, a.err));
       tc_fence_after();
+      const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(MT * buf);
       if (ok) {
+        if constexpr (FRAG) {
+          const float* sr = sa_col + buf * MT + 2 * (lane & 3);
+          // chunk c: 16 lanes x 32 columns; up to four are read together, as a read's latency is several times
+          // what the chunk's FMAs take
+          constexpr int kChunks = MT / 16, kTogether = kChunks < 4 ? kChunks : 4;
+          auto at = [&](int c) { return src + ((uint32_t)(c & 1) << 20) + 32u * (c >> 1); };
 #pragma unroll
-        for (int c = 0; c < MT / 16; ++c) {
+          for (int c0 = 0; c0 < kChunks; c0 += kTogether) {
+            uint32_t p[kTogether][16];
+#pragma unroll
+            for (int k = 0; k < kTogether; ++k) tmem_ld16x32_issue(at(c0 + k), p[k]);
+#pragma unroll
+            for (int k = 0; k < kTogether; ++k) tmem_ld_wait(p[k]);
+#pragma unroll
+            for (int k = 0; k < kTogether; ++k) {
+              const int c = c0 + k;
+#pragma unroll
+              for (int jj = 0; jj < 4; ++jj) {
+                const float2 s2 = *reinterpret_cast<const float2*>(sr + 32 * (c >> 1) + 8 * jj);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float2* t = acc + MT / 4 * (c & 1) + 8 * (c >> 1) + 2 * jj + h;
+                  const uint32_t* v = p[k] + 4 * jj + 2 * h;
+                  *t = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), mul2(s2, dup2(sbv[2 * (c & 1) + h])), *t);
+                }
+              }
+            }
+          }
+        } else {
           float2 p[8];
-          tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(MT * buf + 16 * c), p);
+          tmem_ld16(src, p);
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
-            const float4 s4 = *reinterpret_cast<const float4*>(sa_col + buf * MT + 16 * c + 2 * e);
-            float* t = acc + 16 * c + 2 * e;
-            t[0] = fmaf(p[e].x, sbv * s4.x, t[0]);
-            t[1] = fmaf(p[e].y, sbv * s4.y, t[1]);
-            t[2] = fmaf(p[e + 1].x, sbv * s4.z, t[2]);
-            t[3] = fmaf(p[e + 1].y, sbv * s4.w, t[3]);
+            const float4 s4 = *reinterpret_cast<const float4*>(sa_col + buf * MT + 2 * e);
+            acc[e] = fma2(p[e], mul2(make_float2(s4.x, s4.y), dup2(sbv[0])), acc[e]);
+            acc[e + 1] = fma2(p[e + 1], mul2(make_float2(s4.z, s4.w), dup2(sbv[0])), acc[e + 1]);
           }
         }
       }
@@ -646,36 +747,33 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   // warp meets here, then the totals take their place
   __syncthreads();
   if (warp >= 2) {
-    const int nl = 32 * (warp & 3) + lane;
+    const int nl = 32 * (warp & 3);
+    if constexpr (FRAG) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) total[i * 128 + nl] = acc[i];
+      for (int jj = 0; jj < MT / 8; ++jj) {
+        const int m = 8 * jj + 2 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = acc[MT / 4 * (i >> 1) + 2 * jj + (i & 1)];
+          float* t = total + m * kTotLd + nl + (lane >> 2) + 8 * i;
+          t[0] = v.x;
+          t[kTotLd] = v.y;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < MT / 2; ++i) {
+        total[2 * i * kTotLd + nl + lane] = acc[i].x;
+        total[(2 * i + 1) * kTotLd + nl + lane] = acc[i].y;
+      }
+    }
   }
   if (cs > 1) cluster_sync_all();
   else __syncthreads();
   if (!*abort_flag && warp >= 2) {
-    const int nl = threadIdx.x - 64, n = n0 + nl;
-    const float d = a.d && n < a.N ? a.d[n] : 0.0f;
     const int i0 = MT * rank / cs, i1 = MT * (rank + 1) / cs;
-    uint32_t peer[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) peer[j] = cluster_addr(total, j < cs ? (uint32_t)j : 0u);
-    for (int i = i0; i < i1; ++i) {
-      const int m = m0 + i;
-      if (m >= a.M) break;
-      float z = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < cs) z += ld_cluster(peer[j] + (uint32_t)(i * 128 + nl) * 4u);
-      z += d;
-      if (n < a.N) {
-        if constexpr (F32) {
-          float* p = static_cast<float*>(a.y) + (int64_t)m * a.ldy + n;
-          *p = a.accumulate ? *p + z : z;
-        } else {
-          static_cast<__nv_bfloat16*>(a.y)[(int64_t)m * a.ldy + n] = __float2bfloat16_rn(f8_act<EPI>(z));
-        }
-      }
-    }
+    if (cs <= 2) add_totals<2, 8, EPI, F32>(a, total, cs, n0, m0, i0, i1, warp - 2, lane);
+    else add_totals<8, 2, EPI, F32>(a, total, cs, n0, m0, i0, i1, warp - 2, lane);
   }
   // no CTA leaves while another may read its totals
   if (cs > 1) cluster_sync_all();
@@ -737,7 +835,27 @@ gn_status fp8_run(const void* A, int64_t lda, const void* B, int64_t ldb, Fp8Arg
   if (sms <= 0) return GN_ERR_CUDA;
   const int64_t pairs = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
   CUtensorMap ta, tb, ty;
-  if (a.N > 128 && a.M > 128 && pairs >= sms / 4) {
+  // The split kernel's cluster: as many CTAs as fit at once, with room for the clusters not to divide a GPC's
+  // SMs evenly. Measured at 5120 columns and one row: 12.4 us with clusters of 2 (80 CTAs), 8.1 with 6 (240),
+  // 11.9 with 8 (320: a second wave).
+  auto split = [&](int MT, int64_t* tiles) {
+    *tiles = (int64_t)((a.N + 127) / 128) * ((a.M + MT - 1) / MT);
+    const int64_t slots = (int64_t)((MT == 128 ? 0.9f : 1.7f) * (float)sms), cs = slots / *tiles;
+    return (int)(cs < 1 ? 1 : cs > 8 ? (a.nkb < 8 ? a.nkb : 8) : cs < a.nkb ? cs : a.nkb);
+  };
+  bool pair = a.M > 128 && a.N > 128;
+  if (pair) {
+    // a block of the contraction takes a pair 0.62 us and a split CTA of 128 rows 0.78: the shorter of the
+    // two by waves x blocks (5120 x 5120 weight: 128 rows 15.8 us split, 26 as a pair tile half empty; 200
+    // rows 32 split, 26 in pairs; 333 x 1288 x 5120: 13.1 split by four, 25.4 in pairs)
+    int64_t tiles;
+    const int cs = split(128, &tiles);
+    const int64_t slots = (int64_t)(0.9f * (float)sms);
+    const int64_t pair_cost = 4 * ((pairs + sms / 2 - 1) / (sms / 2)) * a.nkb;
+    const int64_t split_cost = 5 * ((tiles * cs + slots - 1) / slots) * ((a.nkb + cs - 1) / cs);
+    pair = pair_cost <= split_cost;
+  }
+  if (pair) {
     if (!make_code_map(&ta, A, a.M, a.K, lda, 128) || !make_code_map(&tb, B, a.N, a.K, ldb, 128) ||
         !make_y_map(&ty, a.y, a.M, a.N, a.ldy, f32))
       return GN_ERR_CUDA;
@@ -753,9 +871,8 @@ gn_status fp8_run(const void* A, int64_t lda, const void* B, int64_t ldb, Fp8Arg
     return launch_status();
   }
   const int MT = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
-  const int64_t tiles = (int64_t)((a.N + 127) / 128) * ((a.M + MT - 1) / MT);
-  int cs = 1;
-  while (cs < 8 && tiles * cs < 2 * sms && a.nkb >= 4 * cs) cs *= 2;
+  int64_t tiles;
+  int cs = split(MT, &tiles);
   if (!make_code_map(&ta, A, a.M, a.K, lda, (uint32_t)MT) || !make_code_map(&tb, B, a.N, a.K, ldb, 128)) return GN_ERR_CUDA;
   void* kern = MT == 16   ? pick_split<16>(epi, f32)
                : MT == 32 ? pick_split<32>(epi, f32)
