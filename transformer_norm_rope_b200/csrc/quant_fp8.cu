@@ -40,11 +40,9 @@ __device__ __forceinline__ float block_scale(float amax) {
   return amax <= 3.402823466e38f ? quotient(fmaxf(amax, kAmaxFloor), kE4m3Max, 1.0f / kE4m3Max) : __int_as_float(0x7fffffff);
 }
 
-// 1 / s: correctly rounded where the quotient has to be, else the hardware's approximation (1 ulp)
-template <bool EXACT>
-__device__ __forceinline__ float inverse(float s) {
-  return EXACT ? __frcp_rn(s) : __fdividef(1.0f, s);
-}
+// 1 / sqrt(v), rounded twice. One per row or block: next to a value's own roundings the hardware's
+// approximations (2 ulp for all of a row) would move two to three times as many codes.
+__device__ __forceinline__ float inverse_root(float v) { return __frcp_rn(__fsqrt_rn(v)); }
 
 // two codes, lo in the low byte
 __device__ __forceinline__ uint32_t code2(float lo, float hi) {
@@ -52,17 +50,14 @@ __device__ __forceinline__ uint32_t code2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// four codes of v / s, i = 1 / s. EXACT: the rounded quotient; otherwise v i, for values that are themselves
-// fp32 evaluations: one rounding more is no more than they already carry.
-template <bool EXACT>
+// four codes of v / s, i = 1 / s: the quotient on pairs. (v i alone saves an instruction a value and moves
+// two to three times as many codes: 112 us against 121 at 32760 x 5120.)
 __device__ __forceinline__ uint32_t code4(const float* v, float s, float i) {
   const float2 a = make_float2(v[0], v[1]), b = make_float2(v[2], v[3]), ii = dup2(i);
   float2 lo = mul2(a, ii), hi = mul2(b, ii);
-  if constexpr (EXACT) {  // the quotient's last step, on pairs
-    const float2 ns = dup2(-s);
-    lo = fma2(fma2(lo, ns, a), ii, lo);
-    hi = fma2(fma2(hi, ns, b), ii, hi);
-  }
+  const float2 ns = dup2(-s);
+  lo = fma2(fma2(lo, ns, a), ii, lo);
+  hi = fma2(fma2(hi, ns, b), ii, hi);
   return code2(lo.x, lo.y) | code2(hi.x, hi.y) << 16;
 }
 
@@ -110,11 +105,11 @@ __device__ __forceinline__ uint4 load_raw(const T* row, int v, int n) {
 }
 
 // E codes of vector v of a row of n codes
-template <int E, bool EXACT>
+template <int E>
 __device__ __forceinline__ void store_codes(uint8_t* row, int v, int n, const float* f, float s, float i) {
   uint32_t w[E / 4];
 #pragma unroll
-  for (int k = 0; k < E / 4; ++k) w[k] = code4<EXACT>(f + 4 * k, s, i);
+  for (int k = 0; k < E / 4; ++k) w[k] = code4(f + 4 * k, s, i);
   uint8_t* out = row + v * E;
   if ((v + 1) * E <= n) {
     if constexpr (E == 8) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
@@ -136,7 +131,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int v, int n, const fl
 //   * norm_quant_stage_kernel, rows of up to 1024 vectors: one warp per row, which a bulk copy brings to the
 //     warp's own stage in shared memory; the warp reads it there once for the statistics and once for the
 //     codes, so that few registers and twenty warps suffice. At 32760 x 5120 bf16 LayerNorm: a row in the
-//     registers of 160 threads 169 us, in those of one warp (12 warps an SM) 154 us, so: see the table;
+//     registers of 160 threads 169 us, in those of one warp (12 warps an SM) 154 us, so: 110 us (RMSNorm 94, no norm 89);
 //   * norm_quant_row_kernel: one block per row, for longer rows and while there are too few rows to fill
 //     the SMs, where a row's latency counts.
 constexpr int kWarpRows = 16;
@@ -157,7 +152,6 @@ __global__ void __launch_bounds__(32 * kWarpRows, 2)
   constexpr int E = Vec<T>::N, H = E / 2;
   constexpr int L = kBlk / E;  // lanes of a block of values
   constexpr bool FAST = fast_math_for<T>();
-  constexpr bool EXACT = NORM == GN_NORM_NONE && EPI == EPI_NONE;
   constexpr int kGroup = VPT;  // vectors whose scales are made together
   static_assert(VPT == 1 || VPT == 2 || VPT == 4, "a power of two");
   extern __shared__ __align__(16) uint4 params[];  // [1 or 2][32 VPT] vectors: weight, bias
@@ -201,7 +195,7 @@ __global__ void __launch_bounds__(32 * kWarpRows, 2)
 #pragma unroll
         for (int e = 0; e < H; ++e) acc = fma2(f[e], f[e], acc);
       }
-      r = rsqrtf(fmaf(group_sum<32>(acc.x + acc.y), inv_n, eps));
+      r = inverse_root(fmaf(group_sum<32>(acc.x + acc.y), inv_n, eps));
     } else if constexpr (NORM == GN_NORM_LN) {
       float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -238,7 +232,7 @@ __global__ void __launch_bounds__(32 * kWarpRows, 2)
           }
         }
       }
-      r = rsqrtf(fmaf(group_sum<32>(acc.x + acc.y), inv_n, eps));
+      r = inverse_root(fmaf(group_sum<32>(acc.x + acc.y), inv_n, eps));
     }
     if constexpr (NORM != GN_NORM_NONE) {
       keep_packed(raw);
@@ -276,14 +270,14 @@ __global__ void __launch_bounds__(32 * kWarpRows, 2)
         }
       }
       // each lane makes the scale of one of its group's blocks
-      const float s = block_scale(group_max<kGroup, L>(am, lane)), i = inverse<EXACT>(s);
+      const float s = block_scale(group_max<kGroup, L>(am, lane)), i = __frcp_rn(s);
       const int vs = lane + 32 * (k0 + value_of_lane<kGroup, L>(lane));
       if (lane % (L / kGroup) == 0 && vs / L * kBlk < hidden) scale[m * lds + vs / L] = s;
 #pragma unroll
       for (int j = 0; j < kGroup; ++j) {
         const int v = lane + 32 * (k0 + j), src = lane_of_value<kGroup, L>(lane, j);
-        const float ij = __shfl_sync(0xffffffffu, i, src), sj = EXACT ? __shfl_sync(0xffffffffu, s, src) : 0.0f;
-        if (v * E < hidden) store_codes<E, EXACT>(q + m * ldq, v, hidden, f[j], sj, ij);
+        const float ij = __shfl_sync(0xffffffffu, i, src), sj = __shfl_sync(0xffffffffu, s, src);
+        if (v * E < hidden) store_codes<E>(q + m * ldq, v, hidden, f[j], sj, ij);
       }
     }
   }
@@ -300,7 +294,6 @@ __global__ void __launch_bounds__(32 * kStageWarps, 1)
   constexpr int E = Vec<T>::N, H = E / 2;
   constexpr int L = kBlk / E;  // lanes of a block of values
   constexpr bool FAST = fast_math_for<T>();
-  constexpr bool EXACT = NORM == GN_NORM_NONE && EPI == EPI_NONE;
   constexpr int kParams = NORM == GN_NORM_LN ? 2 : NORM == GN_NORM_RMS ? 1 : 0;
   // the parameters, `slot` vectors each, then a row per warp
   extern __shared__ __align__(16) uint4 smem_rows[];
@@ -358,7 +351,7 @@ __global__ void __launch_bounds__(32 * kStageWarps, 1)
 #pragma unroll
         for (int e = 0; e < H; ++e) acc = fma2(f[e], f[e], acc);
       }
-      r = rsqrtf(fmaf(group_sum<32>(acc.x + acc.y), inv_n, eps));
+      r = inverse_root(fmaf(group_sum<32>(acc.x + acc.y), inv_n, eps));
     }
     if constexpr (NORM == GN_NORM_LN) {
       // sums of x - K and (x - K)^2 for a K near the mean (that of the row's first 32 vectors): mean
@@ -408,7 +401,7 @@ __global__ void __launch_bounds__(32 * kStageWarps, 1)
         var = fmaf(-d, d, group_sum<32>(s2.x + s2.y) * inv_n);
       }
       mu = k + d;
-      r = rsqrtf((var < 0.0f ? 0.0f : var) + eps);
+      r = inverse_root((var < 0.0f ? 0.0f : var) + eps);
     }
     if constexpr (NORM != GN_NORM_NONE) {
       if (lane == 0) {
@@ -432,13 +425,16 @@ __global__ void __launch_bounds__(32 * kStageWarps, 1)
         float2 z[H];
         unpack2<T>(stage[v], z);
         if constexpr (NORM != GN_NORM_NONE) {
-          float2 w[H], b[H];
+          float2 w[H];
           unpack2<T>(params[v], w);
-          if constexpr (NORM == GN_NORM_LN) unpack2<T>(params[slot + v], b);
+          if constexpr (NORM == GN_NORM_LN) {
+            float2 b[H];
+            unpack2<T>(params[slot + v], b);
 #pragma unroll
-          for (int e = 0; e < H; ++e) {
-            if constexpr (NORM == GN_NORM_LN) z[e] = fma2(mul2(add2(z[e], dup2(-mu)), dup2(r)), w[e], b[e]);
-            else z[e] = mul2(mul2(z[e], dup2(r)), add2(w[e], gem));
+            for (int e = 0; e < H; ++e) z[e] = fma2(mul2(add2(z[e], dup2(-mu)), dup2(r)), w[e], b[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < H; ++e) z[e] = mul2(mul2(z[e], dup2(r)), add2(w[e], gem));
           }
         }
 #pragma unroll
@@ -449,14 +445,14 @@ __global__ void __launch_bounds__(32 * kStageWarps, 1)
         }
       }
       // each lane makes the scale of one of its group's four blocks
-      const float s = block_scale(group_max<4, L>(am, lane)), i = inverse<EXACT>(s);
+      const float s = block_scale(group_max<4, L>(am, lane)), i = __frcp_rn(s);
       const int vs = lane + 32 * (k0 + value_of_lane<4, L>(lane));
       if (lane % (L / 4) == 0 && (!CHECK || vs / L * kBlk < hidden)) scale[m * lds + vs / L] = s;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int v = lane + 32 * (k0 + j), src = lane_of_value<4, L>(lane, j);
-        const float ij = __shfl_sync(0xffffffffu, i, src), sj = EXACT ? __shfl_sync(0xffffffffu, s, src) : 0.0f;
-        if (!CHECK || v < nvec) store_codes<E, EXACT>(qrow, v, CHECK ? hidden : INT32_MAX, f[j], sj, ij);
+        const float ij = __shfl_sync(0xffffffffu, i, src), sj = __shfl_sync(0xffffffffu, s, src);
+        if (!CHECK || v < nvec) store_codes<E>(qrow, v, CHECK ? hidden : INT32_MAX, f[j], sj, ij);
       }
     };
     int k0 = 0;
@@ -481,7 +477,6 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_quant_row_kernel(c
   constexpr int E = Vec<T>::N;
   constexpr int L = kBlk / E;  // threads of a block of values
   constexpr bool FAST = fast_math_for<T>();
-  constexpr bool EXACT = NORM == GN_NORM_NONE && EPI == EPI_NONE;
   __shared__ float red[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t m = blockIdx.x;
@@ -535,7 +530,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_quant_row_kernel(c
         acc = fma2(d, d, acc);
       }
     }
-    r = rsqrtf(fmaf(total(acc.x + acc.y, 1), inv_n, eps));
+    r = inverse_root(fmaf(total(acc.x + acc.y, 1), inv_n, eps));
     if (t == 0) {
       if (mean && NORM == GN_NORM_LN) mean[m] = mu;
       if (rstd) rstd[m] = r;
@@ -591,7 +586,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_quant_row_kernel(c
     }
   }
   // each lane makes the scale of one of its group's VPT blocks
-  const float s = block_scale(group_max<VPT, L>(am, lane)), i = inverse<EXACT>(s);
+  const float s = block_scale(group_max<VPT, L>(am, lane)), i = __frcp_rn(s);
   {
     const int v = t + value_of_lane<VPT, L>(lane) * team;
     if (lane % (L / VPT) == 0 && v / L * kBlk < hidden) scale[m * lds + v / L] = s;
@@ -599,8 +594,8 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_quant_row_kernel(c
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int v = t + k * team, src = lane_of_value<VPT, L>(lane, k);
-    const float ik = __shfl_sync(0xffffffffu, i, src), sk = EXACT ? __shfl_sync(0xffffffffu, s, src) : 0.0f;
-    if (v * E < hidden) store_codes<E, EXACT>(q + m * ldq, v, hidden, f[k], sk, ik);
+    const float ik = __shfl_sync(0xffffffffu, i, src), sk = __shfl_sync(0xffffffffu, s, src);
+    if (v * E < hidden) store_codes<E>(q + m * ldq, v, hidden, f[k], sk, ik);
   }
 }
 
@@ -632,7 +627,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
   constexpr int L = kBlk / E;         // lanes of a row: 16 or 32
   constexpr int R = 32 / E;           // rows of a thread: 4 or 8
   constexpr bool FAST = fast_math_for<T>();
-  constexpr bool EXACT = !GRAD || EPI == EPI_NONE;
   __shared__ __align__(16) uint8_t bytes[kBlk * kBlk];
   __shared__ __align__(16) float red_max[kTileWarps][kBlk], red_sum[GRAD ? kTileWarps : 1][kBlk];
   __shared__ __align__(16) float col_scale[kBlk], col_inv[kBlk];
@@ -728,7 +722,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
         for (int w = 0; w < kTileWarps; ++w) m = max_nan(m, red_max[w][threadIdx.x]);
         const float s = block_scale(m);
         col_scale[threadIdx.x] = s;
-        col_inv[threadIdx.x] = inverse<EXACT>(s);
+        col_inv[threadIdx.x] = __frcp_rn(s);
         if (threadIdx.x < nc) a.scale_t[(c0 + threadIdx.x) * a.ldst + blockIdx.y] = s;
       }
     }
@@ -741,7 +735,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
       }
     }
   }
-  const float s_all = TILE ? block_scale(all) : 0.0f, i_all = TILE ? inverse<EXACT>(s_all) : 0.0f;
+  const float s_all = TILE ? block_scale(all) : 0.0f, i_all = TILE ? __frcp_rn(s_all) : 0.0f;
   if (TILE && threadIdx.x == 0) {
     if (a.q) a.scale[(int64_t)blockIdx.y * a.lds + blockIdx.x] = s_all;
     if (a.qt) a.scale_t[(int64_t)blockIdx.x * a.ldst + blockIdx.y] = s_all;
@@ -758,7 +752,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
     for (int e = 0; e < E; e += 4) {
       uint32_t w[R], t[4][R / 4];
 #pragma unroll
-      for (int i = 0; i < R; ++i) w[i] = code4<EXACT>(f[i] + e, s_all, i_all);
+      for (int i = 0; i < R; ++i) w[i] = code4(f[i] + e, s_all, i_all);
       if (a.q) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -791,14 +785,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
     }
   } else {
     if (a.q) {  // each lane makes the scale of one of its group's rows
-      const float s = block_scale(group_max<R, L>(rmax, lane)), inv = inverse<EXACT>(s);
+      const float s = block_scale(group_max<R, L>(rmax, lane)), inv = __frcp_rn(s);
       const int ir = row0 + value_of_lane<R, L>(lane);
       if (lane % (L / R) == 0 && ir < nr) a.scale[(r0 + ir) * a.lds + blockIdx.x] = s;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int src = lane_of_value<R, L>(lane, i);
-        const float ii = __shfl_sync(0xffffffffu, inv, src), si = EXACT ? __shfl_sync(0xffffffffu, s, src) : 0.0f;
-        if (row0 + i < nr && lv * E < nc) store_codes<E, EXACT>(a.q + (r0 + row0 + i) * a.ldq + c0, lv, nc, f[i], si, ii);
+        const float ii = __shfl_sync(0xffffffffu, inv, src), si = __shfl_sync(0xffffffffu, s, src);
+        if (row0 + i < nr && lv * E < nc) store_codes<E>(a.q + (r0 + row0 + i) * a.ldq + c0, lv, nc, f[i], si, ii);
       }
     }
     if (a.qt) {
@@ -806,12 +800,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int c = lv * E + e;
-        const float s = EXACT ? col_scale[c] : 0.0f, inv = col_inv[c];
+        const float s = col_scale[c], inv = col_inv[c];
         uint32_t w[R / 4];
 #pragma unroll
         for (int k = 0; k < R / 4; ++k) {
           const float v[4] = {f[4 * k][e], f[4 * k + 1][e], f[4 * k + 2][e], f[4 * k + 3][e]};
-          w[k] = code4<EXACT>(v, s, inv);
+          w[k] = code4(v, s, inv);
         }
         put(c, w);
       }
