@@ -1,0 +1,195 @@
+"""The 8-bit linear layer (fp8_linear): its operators run together, as a layer and behind GroupNorm, against the
+layer's formulas in 64 bits on the values that the codes stand for.
+
+Tolerances. y: half a step of bf16 (2^-8) twice (z and y where an activation follows) plus the product's fp32 sums
+(2^-17 of the sum of |a||b|). Gradients also go through codes: dz is held in codes, so dx and dW differ from the
+formula by up to half an e4m3 step (2^-4, random in sign) of each of its terms; over n terms of one size the 2-norm
+of the sum's error stays within 2^-4 of the 2-norm of the terms' own, sqrt(sum (a b)^2): checked at twice that on
+every element's root mean square, that is on the tensor's 2-norm.
+"""
+import pytest
+import torch
+
+import transformer_norm_rope_b200 as gn
+from transformer_norm_rope_b200 import fp8_linear as fl
+
+
+def act64(z, act):
+    if act == "silu":
+        return z * torch.sigmoid(z)
+    if act == "gelu_tanh":
+        return 0.5 * z * (1 + torch.tanh((2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3)))
+    return z
+
+
+def norm64(x, g, beta, norm, eps, gemma):
+    if norm == "none":
+        return x
+    if norm == "rms":
+        return x * (x.square().mean(-1, keepdim=True) + eps) ** -0.5 * (1 + g if gemma else g)
+    mu = x.mean(-1, keepdim=True)
+    return (x - mu) * ((x - mu).square().mean(-1, keepdim=True) + eps) ** -0.5 * g + beta
+
+
+def values(q, s, tile=False):
+    """what codes stand for, in double"""
+    rows, cols = q.shape
+    sx = s.double().repeat_interleave(128, 1)[:, :cols]
+    if tile:
+        sx = sx.repeat_interleave(128, 0)[:rows]
+    return q.double() * sx
+
+
+def layer(M, N, K, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    t = {"x": 1.5 * r(M, K) + 0.3, "W": r(N, K) / K ** 0.5, "g": 1 + 0.1 * r(K), "beta": 0.1 * r(K), "dy": r(M, N)}
+    t = {k: v.to(torch.bfloat16).cuda() for k, v in t.items()}
+    t["bias"] = (0.3 * r(N)).cuda()
+    return t
+
+
+def rel(a, b):
+    return float((a.double() - b).norm() / b.norm())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "silu", "gelu_tanh"])
+@pytest.mark.parametrize("norm,gemma", [("none", False), ("ln", False), ("rms", False), ("rms", True)])
+@pytest.mark.parametrize("M,N,K", [(1, 256, 512), (37, 136, 264), (300, 520, 648), (1030, 2056, 1304)])
+def test_layer(gpu, M, N, K, norm, gemma, act):
+    t = layer(M, N, K)
+    w = fl.prepare(t["W"])
+    ng, nb = (None, None) if norm == "none" else (t["g"], t["beta"] if norm == "ln" else None)
+    args = dict(norm=norm, g=ng, beta=nb, eps=1e-5, gemma=gemma, act=act)
+    y, mean, rstd, z = fl.forward_keeping_z(t["x"], w, t["bias"], **args)
+    y2, _, _ = fl.forward(t["x"], fl.prepare(t["W"], training=False), t["bias"], **args)
+    q, s, _, _ = gn.norm_quant_fp8(t["x"], ng, nb, 1e-5, norm=norm, gemma=gemma)
+    a, b = values(q, s), values(w.q, w.scale, tile=True)
+    z64 = a @ b.t() + t["bias"].double()
+    acc = 2.0 ** -17 * (a.abs() @ b.abs().t() + t["bias"].double().abs())
+    assert ((z.double() - z64).abs() <= 2.0 ** -8 * z64.abs() + acc).all()
+    v = act64(z64, act)
+    for out in (y, y2):
+        assert ((out.double() - v).abs() <= 2.0 ** -8 * v.abs() + (1.2 * (2.0 ** -8 * z64.abs() + acc) + 2.0 ** -11 * z64.abs() if act != "none" else acc)).all()
+
+    dx, dg, dbeta, dW, dbias = fl.backward(t["x"], w, z, t["dy"], mean=mean, rstd=rstd, **args)
+    # dz from the z that was kept; dW and dxn as the formula gives them on dz and the layer's operands
+    zz = z.double().clone().requires_grad_(True)
+    (dz,) = torch.autograd.grad((act64(zz, act) * t["dy"].double()).sum(), zz)
+    assert ((dbias.double() - dz.sum(0)).abs() <= 2e-5 * dz.abs().sum(0) + 1e-6).all()
+    xn = norm64(t["x"].double(), t["g"].double(), t["beta"].double(), norm, 1e-5, gemma)
+    dW64 = dz.t() @ xn
+    terms = (dz.square().t() @ xn.square()).sum().sqrt()  # 2-norm of all the terms
+    # two operands in codes and xn through bf16: 2^-4 twice, random over the tokens
+    assert (dW.double() - dW64).norm() <= 2 * 2.0 ** -4 * terms * 2 ** 0.5
+    dxn64 = dz @ b
+    xx, gg, bb = (v.double().clone().requires_grad_(True) for v in (t["x"], t["g"], t["beta"]))
+    grads = torch.autograd.grad((norm64(xx, gg, bb, norm, 1e-5, gemma) * dxn64).sum(), (xx, gg, bb), allow_unused=True)
+    dterms = (dz.square() @ b.square()).sum().sqrt()
+    scale = 1.0 if norm == "none" else float((rstd.double().max() * (1 + t["g"].double().abs().max())))
+    assert (dx.double() - grads[0]).norm() <= (2 * 2.0 ** -4 * dterms + 2 * 2.0 ** -8 * dxn64.norm()) * scale
+    if norm != "none":
+        assert (dg.double() - grads[1]).norm() <= (2 * 2.0 ** -4 * dterms + 2 * 2.0 ** -8 * dxn64.norm()) * float(xn.abs().max())
+    if norm == "ln":
+        assert (dbeta.double() - grads[2]).norm() <= (2 * 2.0 ** -4 * dterms + 2 * 2.0 ** -8 * dxn64.norm()) * M ** 0.5
+    else:
+        assert dbeta is None
+    assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
+def test_autograd_function_and_its_graph(gpu):
+    """The autograd form gives the module's gradients; a second layer's captured forward and backward replay to the
+    same bits while the first one's eager graph lives on (of other leaves: a capture of the same leaves' backward
+    would touch state that the eager graph holds)."""
+    t = layer(260, 392, 520)
+    leaves = {k: t[k].clone().requires_grad_(True) for k in ("x", "W", "g", "beta")}
+    bias = t["bias"].bfloat16().requires_grad_(True)
+    y = fl.Fp8LinearFunction.apply(leaves["x"], leaves["W"], bias, leaves["g"], leaves["beta"], "ln", 1e-5, False, "silu")
+    y.backward(t["dy"])
+    w = fl.prepare(t["W"])
+    args = dict(norm="ln", g=t["g"], beta=t["beta"], act="silu")
+    y2, mean, rstd, z = fl.forward_keeping_z(t["x"], w, bias.detach().float(), **args)
+    dx, dg, dbeta, dW, dbias = fl.backward(t["x"], w, z, t["dy"], mean=mean, rstd=rstd, **args)
+    assert torch.equal(y.detach(), y2) and torch.equal(leaves["x"].grad, dx) and torch.equal(leaves["W"].grad, dW.bfloat16())
+    assert torch.equal(leaves["g"].grad, dg.bfloat16()) and torch.equal(leaves["beta"].grad, dbeta.bfloat16())
+    assert torch.equal(bias.grad, dbias.bfloat16())
+
+    def step():
+        y, mean, rstd, z = fl.forward_keeping_z(t["x"], w, t["bias"], **args)
+        return (y,) + tuple(fl.backward(t["x"], w, z, t["dy"], mean=mean, rstd=rstd, **args))
+
+    want = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_gradients_against_differences(gpu):
+    """With the codes fixed the layer is linear in them: the directional derivative of sum(y dy) along the bias is
+    exact up to bf16 (2^-8 of the magnitudes), and dW along a direction that keeps every code's block scale matches
+    the difference of two forwards within the codes' rounding."""
+    M, N, K = 64, 128, 256
+    t = layer(M, N, K, seed=3)
+    w = fl.prepare(t["W"])
+    f = lambda d: (fl.forward(t["x"], w, d, act="silu")[0].double() * t["dy"].double()).sum()  # noqa: E731
+    y, _, _, z = fl.forward_keeping_z(t["x"], w, t["bias"], act="silu")
+    _, _, _, dW, dbias = fl.backward(t["x"], w, z, t["dy"], act="silu")
+    v, h = torch.randn(N, device="cuda"), 0.25
+    num = (f(t["bias"] + h * v) - f(t["bias"] - h * v)) / (2 * h)
+    ana = (dbias.double() * v.double()).sum()
+    mags = (t["dy"].double().abs() * (y.double().abs() * 2.0 ** -8 / h + h ** 2 * 0.2)).square().sum().sqrt() * v.double().abs().max() ** 3
+    assert (num - ana).abs() <= 2 * mags + 0.02 * (dbias.double().norm() * v.double().norm()) / N ** 0.5
+    # along W: the layer is linear in W's values, so the derivative of sum(z dy) along V is sum((a V^T) dy)
+    q, s, _, _ = gn.norm_quant_fp8(t["x"], norm="none")
+    V = torch.randn(N, K, device="cuda", dtype=torch.float64)
+    zz = z.double().clone().requires_grad_(True)
+    (dz,) = torch.autograd.grad((act64(zz, "silu") * t["dy"].double()).sum(), zz)
+    num = ((values(q, s) @ V.t()) * dz).sum()
+    ana = (dW.double() * V).sum()
+    assert (num - ana).abs() <= 4 * 2.0 ** -4 * 2 ** 0.5 * (dz.square().t() @ t["x"].double().square()).sum().sqrt()
+
+
+@pytest.mark.gpu
+def test_groupnorm_in_front_of_the_layer(gpu):
+    """An image block's projection: GroupNorm with SiLU over [N, H, W, C], then the 8-bit layer on its positions,
+    and the way back to the image's gradient."""
+    N, H, W, C, F, G = 2, 12, 11, 160, 264, 16
+    g = torch.Generator().manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    x, gw, gb, Wt, dy = r(N, H, W, C), 1 + 0.1 * r(C), 0.1 * r(C), r(F, C) / C ** 0.5, r(N * H * W, F)
+    w = fl.prepare(Wt)
+    n, mean, rstd = gn.groupnorm_fwd(x, G, gw, gb, epilogue="silu")
+    y, _, _, z = fl.forward_keeping_z(n.view(-1, C), w)
+    dn, _, _, dW, _ = fl.backward(n.view(-1, C), w, z, dy, want_dbias=False)
+    dx, dgw, dgb = gn.groupnorm_bwd(x, G, gw, gb, mean, rstd, dn.view_as(n), epilogue="silu")
+
+    xx, ww, bb, W64 = (v.double().clone().requires_grad_(True) for v in (x, gw, gb, Wt))
+    xg = xx.reshape(N, H * W, G, C // G)
+    mu = xg.mean((1, 3), keepdim=True)
+    zz = ((xg - mu) * (((xg - mu) ** 2).mean((1, 3), keepdim=True) + 1e-5) ** -0.5).reshape(N * H * W, C) * ww + bb
+    out = (zz * torch.sigmoid(zz)) @ W64.t()
+    want = torch.autograd.grad((out * dy.double()).sum(), (xx, ww, bb, W64))
+    # every operand of the three products has gone through codes: 2^-4 of each term at most, two operands, random
+    for got, ref in ((y, out.detach()), (dx, want[0]), (dgw, want[1]), (dgb, want[2]), (dW, want[3])):
+        assert rel(got, ref) <= 2 * 2.0 ** -4 * 2 ** 0.5
+    assert gpu.device_error() == 0
+
+
+def test_helper_refusals(monkeypatch):
+    w = fl.Weight(torch.zeros(1), torch.zeros(1), None, None)
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="transpose"):
+        fl.backward(x, w, x, x)
+    w = fl.Weight(torch.zeros(1), torch.zeros(1), torch.zeros(1), torch.zeros(1))
+    with pytest.raises(ValueError, match="norm"):
+        fl.backward(x, w, x, x, norm="group")
+    with pytest.raises(ValueError, match="norm weight"):
+        fl.backward(x, w, x, x, norm="rms")
