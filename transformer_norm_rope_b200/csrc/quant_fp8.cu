@@ -606,7 +606,8 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_quant_row_kernel(c
 // lanes (amax by shuffles, codes stored from registers, 128 bytes a row), and a column's is the warp's
 // rows and then the sixteen warps (shared memory). The transposed codes of a thread are R consecutive
 // bytes of each of its columns: they meet in a 16 KiB byte tile (16-byte chunk j of column c at j ^ key(c),
-// so that neither side conflicts) and leave as 128-byte runs. Both ways and the bias gradient in one read:
+// so that neither side conflicts) and leave as 128-byte runs. A block walks over tiles and has the next
+// one's vectors copied to each thread's own place in shared memory while it works on this one. Both ways and the bias gradient in one read:
 // 6 bytes a value for a bf16 gradient. Bound by HBM.
 constexpr int kTileThreads = 512, kTileWarps = 16;
 
@@ -619,7 +620,13 @@ struct QuantArgs {
   float* scale_t;
   float* colsum;
   int64_t rows, cols, ldx, lddy, ldq, lds, ldqt, ldst;
+  unsigned row_tiles, col_tiles;
 };
+
+// 16 bytes of a row into this thread's place in shared memory, `bytes` of them read and the rest zero
+__device__ __forceinline__ void copy16(uint4* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
 
 template <typename T, int EPI, bool GRAD, bool TILE>
 __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const QuantArgs a) {
@@ -627,207 +634,220 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
   constexpr int L = kBlk / E;         // lanes of a row: 16 or 32
   constexpr int R = 32 / E;           // rows of a thread: 4 or 8
   constexpr bool FAST = fast_math_for<T>();
-  __shared__ __align__(16) uint8_t bytes[kBlk * kBlk];
-  __shared__ __align__(16) float red_max[kTileWarps][kBlk], red_sum[GRAD ? kTileWarps : 1][kBlk];
-  __shared__ __align__(16) float col_scale[kBlk], col_inv[kBlk];
+  // the next tile, each thread's own vectors: [x and dy][R][threads]; then what the block shares
+  extern __shared__ __align__(16) uint4 ahead[];
+  uint8_t* bytes = reinterpret_cast<uint8_t*>(ahead + (GRAD ? 2 : 1) * R * kTileThreads);
+  float(*red_max)[kBlk] = reinterpret_cast<float(*)[kBlk]>(bytes + kBlk * kBlk);
+  float* col_scale = red_max[kTileWarps];
+  float* col_inv = col_scale + kBlk;
+  float(*red_sum)[kBlk] = reinterpret_cast<float(*)[kBlk]>(col_inv + kBlk);  // GRAD
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t r0 = (int64_t)blockIdx.y * kBlk, c0 = (int64_t)blockIdx.x * kBlk;
-  const int nr = a.rows - r0 < kBlk ? (int)(a.rows - r0) : kBlk;
-  const int nc = a.cols - c0 < kBlk ? (int)(a.cols - c0) : kBlk;
   const int lv = lane % L;                          // vector of the row
   const int row0 = 8 * warp + (lane / L) * R;       // first row of the thread
-  const T* x = static_cast<const T*>(a.x) + r0 * a.ldx + c0;
-  const T* dy = GRAD ? static_cast<const T*>(a.dy) + r0 * a.lddy + c0 : nullptr;
-  // whole tiles: every load of the thread is issued before the first value is used
-  const bool whole = nr == kBlk && nc == kBlk;
-  uint4 raw[R], rawd[GRAD ? R : 1];
-  if (whole) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) raw[i] = ld_stream(x + (row0 + i) * a.ldx + lv * E);
-    if constexpr (GRAD) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) rawd[i] = ld_stream(dy + (row0 + i) * a.lddy + lv * E);
-    }
-  } else {
+  const unsigned tiles = (unsigned)a.col_tiles * (unsigned)a.row_tiles;
+  auto fetch = [&](unsigned tile) {
+    const unsigned ty = tile / a.col_tiles;
+    const int64_t r0 = (int64_t)ty * kBlk, c = (int64_t)(tile - ty * a.col_tiles) * kBlk + lv * E;
+    const int64_t left = (a.cols - c) * (int64_t)sizeof(T);
+    const int most = left <= 0 ? 0 : left < 16 ? (int)left : 16;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      raw[i] = load_raw<T>(x + (row0 + i) * a.ldx, lv, row0 + i < nr ? nc : 0);
-      if constexpr (GRAD) rawd[i] = load_raw<T>(dy + (row0 + i) * a.lddy, lv, row0 + i < nr ? nc : 0);
+      const int64_t r = r0 + row0 + i;
+      const bool in = r < a.rows && most > 0;
+      copy16(ahead + i * kTileThreads + threadIdx.x, static_cast<const T*>(a.x) + (in ? r * a.ldx + c : 0), in ? most : 0);
+      if constexpr (GRAD)
+        copy16(ahead + (R + i) * kTileThreads + threadIdx.x, static_cast<const T*>(a.dy) + (in ? r * a.lddy + c : 0),
+               in ? most : 0);
     }
-  }
-  float f[R][E];
+  };
+  fetch(blockIdx.x);
+  for (unsigned tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const unsigned tile_y = tile / a.col_tiles, tile_x = tile - tile_y * a.col_tiles;
+    const int64_t r0 = (int64_t)tile_y * kBlk, c0 = (int64_t)tile_x * kBlk;
+    const int nr = a.rows - r0 < kBlk ? (int)(a.rows - r0) : kBlk;
+    const int nc = a.cols - c0 < kBlk ? (int)(a.cols - c0) : kBlk;
+    uint4 raw[R], rawd[GRAD ? R : 1];
+    asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    Vec<T>::unpack(raw[i], f[i]);
-    if constexpr (GRAD) {  // past the last row and column z and dy are 0: 0 * act'(0) = 0
-      float d[E];
-      Vec<T>::unpack(rawd[i], d);
+    for (int i = 0; i < R; ++i) {
+      raw[i] = ahead[i * kTileThreads + threadIdx.x];
+      if constexpr (GRAD) rawd[i] = ahead[(R + i) * kTileThreads + threadIdx.x];
+    }
+    if (tile + gridDim.x < tiles) fetch(tile + gridDim.x);
+    float f[R][E];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = mul2(make_float2(d[e], d[e + 1]), act_grad_pair<EPI, FAST>(make_float2(f[i][e], f[i][e + 1])));
-        f[i][e] = v.x, f[i][e + 1] = v.y;
+    for (int i = 0; i < R; ++i) {
+      Vec<T>::unpack(raw[i], f[i]);
+      if constexpr (GRAD) {  // past the last row and column z and dy are 0: 0 * act'(0) = 0
+        float d[E];
+        Vec<T>::unpack(rawd[i], d);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = mul2(make_float2(d[e], d[e + 1]), act_grad_pair<EPI, FAST>(make_float2(f[i][e], f[i][e + 1])));
+          f[i][e] = v.x, f[i][e + 1] = v.y;
+        }
       }
     }
-  }
-  float cmax[E], csum[E];
+    float cmax[E], csum[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) cmax[e] = csum[e] = 0.0f;
-  float rmax[R];
+    for (int e = 0; e < E; ++e) cmax[e] = csum[e] = 0.0f;
+    float rmax[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    rmax[i] = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float m = fabsf(f[i][e]);
-      rmax[i] = max_nan(rmax[i], m);
-      cmax[e] = max_nan(cmax[e], m);
-      if constexpr (GRAD) csum[e] += f[i][e];
-    }
-  }
-  float all = 0.0f;
-  if (a.qt || TILE || (GRAD && a.colsum)) {
-    if constexpr (L == 16) {
+    for (int i = 0; i < R; ++i) {
+      rmax[i] = 0.0f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        cmax[e] = max_nan(cmax[e], __shfl_xor_sync(0xffffffffu, cmax[e], 16));
-        if constexpr (GRAD) csum[e] += __shfl_xor_sync(0xffffffffu, csum[e], 16);
+        const float m = fabsf(f[i][e]);
+        rmax[i] = max_nan(rmax[i], m);
+        cmax[e] = max_nan(cmax[e], m);
+        if constexpr (GRAD) csum[e] += f[i][e];
       }
     }
-    if constexpr (TILE) {
-      float m = cmax[0];
+    float all = 0.0f;
+    if (a.qt || TILE || (GRAD && a.colsum)) {
+      if constexpr (L == 16) {
 #pragma unroll
-      for (int e = 1; e < E; ++e) m = max_nan(m, cmax[e]);
+        for (int e = 0; e < E; ++e) {
+          cmax[e] = max_nan(cmax[e], __shfl_xor_sync(0xffffffffu, cmax[e], 16));
+          if constexpr (GRAD) csum[e] += __shfl_xor_sync(0xffffffffu, csum[e], 16);
+        }
+      }
+      if constexpr (TILE) {
+        float m = cmax[0];
 #pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (lane == 0) red_max[0][warp] = m;
-    } else if (lane < L) {
+        for (int e = 1; e < E; ++e) m = max_nan(m, cmax[e]);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) red_max[0][warp] = m;
+      } else if (lane < L) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          *reinterpret_cast<float4*>(&red_max[warp][lv * E + e]) = make_float4(cmax[e], cmax[e + 1], cmax[e + 2], cmax[e + 3]);
+          if constexpr (GRAD)
+            *reinterpret_cast<float4*>(&red_sum[warp][lv * E + e]) = make_float4(csum[e], csum[e + 1], csum[e + 2], csum[e + 3]);
+        }
+      }
+      __syncthreads();
+      if constexpr (TILE) {
+#pragma unroll
+        for (int w = 0; w < kTileWarps; w += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(&red_max[0][w]);
+          all = max_nan(all, max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w)));
+        }
+      } else if (a.qt) {  // a thread per column makes its scale
+        if (threadIdx.x < kBlk) {
+          float m = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kTileWarps; ++w) m = max_nan(m, red_max[w][threadIdx.x]);
+          const float s = block_scale(m);
+          col_scale[threadIdx.x] = s;
+          col_inv[threadIdx.x] = __frcp_rn(s);
+          if (threadIdx.x < nc) a.scale_t[(c0 + threadIdx.x) * a.ldst + tile_y] = s;
+        }
+      }
+      if constexpr (GRAD) {
+        if (a.colsum && threadIdx.x < nc) {
+          float t = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kTileWarps; ++w) t += red_sum[w][threadIdx.x];
+          a.colsum[(int64_t)tile_y * a.cols + c0 + threadIdx.x] = t;
+        }
+      }
+    }
+    const float s_all = TILE ? block_scale(all) : 0.0f, i_all = TILE ? __frcp_rn(s_all) : 0.0f;
+    if (TILE && threadIdx.x == 0) {
+      if (a.q) a.scale[(int64_t)tile_y * a.lds + tile_x] = s_all;
+      if (a.qt) a.scale_t[(int64_t)tile_x * a.ldst + tile_y] = s_all;
+    }
+    // where R codes of column c (vector lv of the row) go: chunk row / 16 of the column; its 8-byte halves change
+    // places on every other eight vectors
+    auto put = [&](int c, const uint32_t* w) {
+      uint8_t* at = bytes + c * kBlk + (((warp >> 1) ^ (lv & 7)) << 4) + 8 * ((warp & 1) ^ ((lv >> 3) & 1));
+      if constexpr (R == 4) *reinterpret_cast<uint32_t*>(at + 4 * (lane / L)) = w[0];
+      else *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+    };
+    if constexpr (TILE) {  // one scale: the codes are made once and their bytes transposed four by four
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
-        *reinterpret_cast<float4*>(&red_max[warp][lv * E + e]) = make_float4(cmax[e], cmax[e + 1], cmax[e + 2], cmax[e + 3]);
-        if constexpr (GRAD)
-          *reinterpret_cast<float4*>(&red_sum[warp][lv * E + e]) = make_float4(csum[e], csum[e + 1], csum[e + 2], csum[e + 3]);
+        uint32_t w[R], t[4][R / 4];
+#pragma unroll
+        for (int i = 0; i < R; ++i) w[i] = code4(f[i] + e, s_all, i_all);
+        if (a.q) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const int c = lv * E + e;
+            if (row0 + i >= nr || c >= nc) continue;
+            uint8_t* out = a.q + (r0 + row0 + i) * a.ldq + c0 + c;
+            if (c + 4 <= nc) {
+              *reinterpret_cast<uint32_t*>(out) = w[i];
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (c + k < nc) out[k] = (uint8_t)(w[i] >> (8 * k));
+            }
+          }
+        }
+        if (a.qt) {
+#pragma unroll
+          for (int k = 0; k < R / 4; ++k) {
+            const uint32_t *u = w + 4 * k;
+            const uint32_t p = __byte_perm(u[0], u[1], 0x5140), q = __byte_perm(u[2], u[3], 0x5140);
+            const uint32_t x = __byte_perm(u[0], u[1], 0x7362), y = __byte_perm(u[2], u[3], 0x7362);
+            t[0][k] = __byte_perm(p, q, 0x5410);
+            t[1][k] = __byte_perm(p, q, 0x7632);
+            t[2][k] = __byte_perm(x, y, 0x5410);
+            t[3][k] = __byte_perm(x, y, 0x7632);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) put(lv * E + e + k, t[k]);
+        }
       }
-    }
-    __syncthreads();
-    if constexpr (TILE) {
-#pragma unroll
-      for (int w = 0; w < kTileWarps; w += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(&red_max[0][w]);
-        all = max_nan(all, max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w)));
-      }
-    } else if (a.qt) {  // a thread per column makes its scale
-      if (threadIdx.x < kBlk) {
-        float m = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kTileWarps; ++w) m = max_nan(m, red_max[w][threadIdx.x]);
-        const float s = block_scale(m);
-        col_scale[threadIdx.x] = s;
-        col_inv[threadIdx.x] = __frcp_rn(s);
-        if (threadIdx.x < nc) a.scale_t[(c0 + threadIdx.x) * a.ldst + blockIdx.y] = s;
-      }
-    }
-    if constexpr (GRAD) {
-      if (a.colsum && threadIdx.x < nc) {
-        float t = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kTileWarps; ++w) t += red_sum[w][threadIdx.x];
-        a.colsum[(int64_t)blockIdx.y * a.cols + c0 + threadIdx.x] = t;
-      }
-    }
-  }
-  const float s_all = TILE ? block_scale(all) : 0.0f, i_all = TILE ? __frcp_rn(s_all) : 0.0f;
-  if (TILE && threadIdx.x == 0) {
-    if (a.q) a.scale[(int64_t)blockIdx.y * a.lds + blockIdx.x] = s_all;
-    if (a.qt) a.scale_t[(int64_t)blockIdx.x * a.ldst + blockIdx.y] = s_all;
-  }
-  // where R codes of column c (vector lv of the row) go: chunk row / 16 of the column; its 8-byte halves change
-  // places on every other eight vectors
-  auto put = [&](int c, const uint32_t* w) {
-    uint8_t* at = bytes + c * kBlk + (((warp >> 1) ^ (lv & 7)) << 4) + 8 * ((warp & 1) ^ ((lv >> 3) & 1));
-    if constexpr (R == 4) *reinterpret_cast<uint32_t*>(at + 4 * (lane / L)) = w[0];
-    else *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-  };
-  if constexpr (TILE) {  // one scale: the codes are made once and their bytes transposed four by four
-#pragma unroll
-    for (int e = 0; e < E; e += 4) {
-      uint32_t w[R], t[4][R / 4];
-#pragma unroll
-      for (int i = 0; i < R; ++i) w[i] = code4(f[i] + e, s_all, i_all);
-      if (a.q) {
+    } else {
+      if (a.q) {  // each lane makes the scale of one of its group's rows
+        const float s = block_scale(group_max<R, L>(rmax, lane)), inv = __frcp_rn(s);
+        const int ir = row0 + value_of_lane<R, L>(lane);
+        if (lane % (L / R) == 0 && ir < nr) a.scale[(r0 + ir) * a.lds + tile_x] = s;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-          const int c = lv * E + e;
-          if (row0 + i >= nr || c >= nc) continue;
-          uint8_t* out = a.q + (r0 + row0 + i) * a.ldq + c0 + c;
-          if (c + 4 <= nc) {
-            *reinterpret_cast<uint32_t*>(out) = w[i];
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (c + k < nc) out[k] = (uint8_t)(w[i] >> (8 * k));
-          }
+          const int src = lane_of_value<R, L>(lane, i);
+          const float ii = __shfl_sync(0xffffffffu, inv, src), si = __shfl_sync(0xffffffffu, s, src);
+          if (row0 + i < nr && lv * E < nc) store_codes<E>(a.q + (r0 + row0 + i) * a.ldq + c0, lv, nc, f[i], si, ii);
         }
       }
       if (a.qt) {
+        __syncthreads();  // the columns' scales
 #pragma unroll
-        for (int k = 0; k < R / 4; ++k) {
-          const uint32_t *u = w + 4 * k;
-          const uint32_t p = __byte_perm(u[0], u[1], 0x5140), q = __byte_perm(u[2], u[3], 0x5140);
-          const uint32_t x = __byte_perm(u[0], u[1], 0x7362), y = __byte_perm(u[2], u[3], 0x7362);
-          t[0][k] = __byte_perm(p, q, 0x5410);
-          t[1][k] = __byte_perm(p, q, 0x7632);
-          t[2][k] = __byte_perm(x, y, 0x5410);
-          t[3][k] = __byte_perm(x, y, 0x7632);
+        for (int e = 0; e < E; ++e) {
+          const int c = lv * E + e;
+          const float s = col_scale[c], inv = col_inv[c];
+          uint32_t w[R / 4];
+#pragma unroll
+          for (int k = 0; k < R / 4; ++k) {
+            const float v[4] = {f[4 * k][e], f[4 * k + 1][e], f[4 * k + 2][e], f[4 * k + 3][e]};
+            w[k] = code4(v, s, inv);
+          }
+          put(c, w);
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) put(lv * E + e + k, t[k]);
       }
     }
-  } else {
-    if (a.q) {  // each lane makes the scale of one of its group's rows
-      const float s = block_scale(group_max<R, L>(rmax, lane)), inv = __frcp_rn(s);
-      const int ir = row0 + value_of_lane<R, L>(lane);
-      if (lane % (L / R) == 0 && ir < nr) a.scale[(r0 + ir) * a.lds + blockIdx.x] = s;
+    __syncthreads();
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int src = lane_of_value<R, L>(lane, i);
-        const float ii = __shfl_sync(0xffffffffu, inv, src), si = __shfl_sync(0xffffffffu, s, src);
-        if (row0 + i < nr && lv * E < nc) store_codes<E>(a.q + (r0 + row0 + i) * a.ldq + c0, lv, nc, f[i], si, ii);
+    for (int it = 0; it < kBlk * 8 / kTileThreads; ++it) {
+      const int idx = it * kTileThreads + threadIdx.x, c = idx >> 3, j = idx & 7;
+      if (!a.qt || c >= nc || 16 * j >= nr) continue;
+      uint4 v = *reinterpret_cast<const uint4*>(bytes + c * kBlk + ((j ^ ((c / E) & 7)) << 4));
+      if ((c / E) & 8) v = make_uint4(v.z, v.w, v.x, v.y);
+      uint8_t* out = a.qt + (c0 + c) * a.ldqt + r0 + 16 * j;
+      if (16 * j + 16 <= nr) {
+        *reinterpret_cast<uint4*>(out) = v;
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (16 * j + k < nr) out[k] = (uint8_t)(w[k / 4] >> (8 * (k % 4)));
       }
     }
-    if (a.qt) {
-      __syncthreads();  // the columns' scales
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = lv * E + e;
-        const float s = col_scale[c], inv = col_inv[c];
-        uint32_t w[R / 4];
-#pragma unroll
-        for (int k = 0; k < R / 4; ++k) {
-          const float v[4] = {f[4 * k][e], f[4 * k + 1][e], f[4 * k + 2][e], f[4 * k + 3][e]};
-          w[k] = code4(v, s, inv);
-        }
-        put(c, w);
-      }
-    }
-  }
-  if (!a.qt) return;
-  __syncthreads();
-#pragma unroll
-  for (int it = 0; it < kBlk * 8 / kTileThreads; ++it) {
-    const int idx = it * kTileThreads + threadIdx.x, c = idx >> 3, j = idx & 7;
-    if (c >= nc || 16 * j >= nr) continue;
-    uint4 v = *reinterpret_cast<const uint4*>(bytes + c * kBlk + ((j ^ ((c / E) & 7)) << 4));
-    if ((c / E) & 8) v = make_uint4(v.z, v.w, v.x, v.y);
-    uint8_t* out = a.qt + (c0 + c) * a.ldqt + r0 + 16 * j;
-    if (16 * j + 16 <= nr) {
-      *reinterpret_cast<uint4*>(out) = v;
-    } else {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (16 * j + k < nr) out[k] = (uint8_t)(w[k / 4] >> (8 * (k % 4)));
-    }
+    __syncthreads();  // the next tile's sums and bytes take these places
   }
 }
 
@@ -959,12 +979,17 @@ extern "C" gn_status gn_quant_fp8(const void* x, const void* dy, void* q, float*
   if (db && (!ws || ws_bytes < gn_quant_fp8_workspace(rows, cols))) return GN_ERR_WORKSPACE;
   if (db && !aligned16(ws)) return GN_ERR_ALIGN;
   QuantArgs a{x, dy, static_cast<uint8_t*>(q), scale, static_cast<uint8_t*>(qt), scale_t,
-              db ? static_cast<float*>(ws) : nullptr, rows, cols, ld_x, ld_dy, ld_q, ld_s, ld_qt, ld_st};
+              db ? static_cast<float*>(ws) : nullptr, rows, cols, ld_x, ld_dy, ld_q, ld_s, ld_qt, ld_st,
+              (unsigned)blocks_of(rows), (unsigned)blocks_of(cols)};
   void* kern = dt == GN_BF16 ? pick_tile<__nv_bfloat16>(epi, dy != nullptr, tile) : pick_tile<float>(epi, dy != nullptr, tile);
-  if (!kernel_attrs(kern, 0)) return GN_ERR_CUDA;
+  const size_t smem = (size_t)kTileThreads * (dt == GN_BF16 ? 4 : 8) * 16 * (dy ? 2 : 1) + kBlk * kBlk +
+                      (kTileWarps * (dy ? 2 : 1) + 2) * kBlk * 4;
+  const int most = persistent_grid(kern, kTileThreads, smem, 0);
+  if (most <= 0) return GN_ERR_CUDA;
+  const int64_t tiles = blocks_of(rows) * blocks_of(cols);
+  if (tiles > INT32_MAX) return GN_ERR_SHAPE;  // far above any device's memory
   void* args[] = {&a};
-  if (cudaLaunchKernel(kern, dim3((unsigned)blocks_of(cols), (unsigned)blocks_of(rows)), dim3(kTileThreads), args, 0,
-                       s) != cudaSuccess)
+  if (cudaLaunchKernel(kern, dim3((unsigned)(tiles < most ? tiles : most)), dim3(kTileThreads), args, smem, s) != cudaSuccess)
     return GN_ERR_CUDA;
   count_launches(1);
   const gn_status st = launch_status();
