@@ -12,8 +12,8 @@
 //
 // Images whose groups fit on chip are read once (the resident kernels, further down). Longer ones take
 // two passes: a pass over slabs of positions that reduces every channel of the slab
-// (gn_stats_kernel, gn_bwd_sums_kernel), a small kernel that joins the slabs and the channels of a
-// group in a fixed order, and an elementwise pass. A thread keeps one 16-byte vector of channels and
+// (gn_stats_kernel, gn_bwd_sums_kernel), a small kernel that joins the slabs in a fixed order (and
+// in the backward the channels of a group), and an elementwise pass. A thread keeps one 16-byte vector of channels and
 // walks down the positions, so its per-channel sums and parameters stay in registers and every warp
 // access covers whole runs of a row. The forward's sums are (mean, centred sum of squares) per
 // channel, taken around a value of the slab and joined with Chan's update: no E[x^2] - E[x]^2 cancellation.
@@ -28,8 +28,8 @@ namespace {
 
 constexpr int kThreads = 256;
 // A thread's next positions are on their way, by asynchronous copies to its own places in shared memory, while
-// it works on one: kRing 16-byte vectors, in the backward half of them of x and half of dy. (4 x 65536 x 512 bf16: 156 us forward,
-// 224 backward; double-buffered in registers 192 and 298.)
+// it works on one: kRing 16-byte vectors, in the backward half of them of x and half of dy. (4 x 65536 x 512 bf16:
+// 158 us forward, 224 backward; double-buffered in registers 192 and 298.)
 constexpr int kRing = 8;
 // blocks on an SM, by registers: a thread of fp32 images has half the channels of a bf16 one
 template <typename T>
@@ -153,7 +153,8 @@ struct Place {
 };
 
 // ---------------------------------------------------------------- forward: slab statistics
-// part[n][chunk][c] = (mean, centred sum of squares) of channel c over the slab.
+// part[n][chunk][slot] = (mean, centred sum of squares) over the slab of the channels that a group has in a
+// column tile; slot = tile + group (neighbouring tiles share at most one group).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kFwdPerSm<T>) gn_stats_kernel(const T* __restrict__ x, int64_t ldx, GnShape g,
                                                             float2* __restrict__ part) {
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm<T>) gn_stats_kernel(const 
   float* sm_mean = reinterpret_cast<float*>(ring);  // the copies have all been read by then
   float* sm_m2 = sm_mean + kThreads * E;
   float* sm_cnt = sm_m2 + kThreads * E;
-  static_assert(sizeof(uint4) * kRing >= 4 * (2 * E + 1), "the sums fit the ring");
+  static_assert(sizeof(uint4) * kRing * kThreads >= 4 * (kThreads * (2 * E + 1) + 2 * 64 * E), "the sums fit the ring");
   const Place p = Place::make<E>(g);
   // sums of x - K and (x - K)^2 per channel, K the thread's first value: mean = K + s1 / n, squares
   // = s2 - s1^2 / n, which loses at most four bits while s1^2 / n <= 16 squares; where the first value is
@@ -230,9 +231,11 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm<T>) gn_stats_kernel(const 
   sm_cnt[threadIdx.x] = cnt;
   __syncthreads();
   // channel j of the tile: merge the rl threads that hold it, in order
-  for (int j = threadIdx.x; j < g.tv * E; j += kThreads) {
-    const int c = (blockIdx.x % g.tiles) * g.tv * E + j;
-    if (c >= g.C) continue;
+  float* ch_mean = sm_cnt + kThreads;
+  float* ch_m2 = ch_mean + g.tv * E;
+  const int tile = blockIdx.x % g.tiles, c_lo = tile * g.tv * E;
+  const int nch = g.C - c_lo < g.tv * E ? g.C - c_lo : g.tv * E;
+  for (int j = threadIdx.x; j < nch; j += kThreads) {
     float mu = 0.0f, q = 0.0f, n = 0.0f;
     for (int k = 0; k < g.rl; ++k) {
       const int t = k * g.tv + j / E;
@@ -243,64 +246,99 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm<T>) gn_stats_kernel(const 
       q += fmaf(dl * dl, n * (nk / tot), sm_m2[t * E + j % E]);
       n = tot;
     }
-    part[((int64_t)p.n * g.chunks + p.chunk) * g.C + c] = make_float2(mu, q);
+    ch_mean[j] = mu;
+    ch_m2[j] = q;
+  }
+  __syncthreads();
+  // the tile's part of each group: as many neighbouring lanes as it has channels, a warp at most
+  const int g_lo = c_lo / g.P, groups = (c_lo + nch - 1) / g.P - g_lo + 1;
+  int team = 32;
+  while (team > 1 && team / 2 >= g.P) team /= 2;
+  const int lane = threadIdx.x & (team - 1), per = kThreads / team;
+  const float rows = (float)(p.r1 - p.r0);
+  auto team_sum = [&](float v) {
+    for (int d = team / 2; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+  };
+  for (int i = 0; i < groups; i += per) {  // the same number of turns for every lane
+    const int gi = g_lo + i + threadIdx.x / team;
+    int a = gi * g.P - c_lo, b = a + g.P;
+    a = a > 0 ? a : 0;
+    b = b < nch ? b : nch;
+    float t = 0.0f, q = 0.0f;
+    for (int j = a + lane; j < b; j += team) t += ch_mean[j];
+    const float mu = team_sum(t) / (float)(b - a);
+    for (int j = a + lane; j < b; j += team) q += fmaf(rows * (ch_mean[j] - mu), ch_mean[j] - mu, ch_m2[j]);
+    q = team_sum(q);
+    if (lane == 0 && b > a)
+      part[((int64_t)p.n * g.chunks + p.chunk) * (g.G + g.tiles - 1) + tile + gi] = make_float2(mu, q);
   }
 }
 
-constexpr int kJoin = 1024;  // threads of the joins: the partial sums are few and a join waits on their latency
+constexpr int kJoin = 1024, kJoinFwd = 256;
 
-__device__ __forceinline__ float block_sum(float v, float* red) {  // kJoin threads, fixed order
+template <int THREADS>
+__device__ __forceinline__ float block_sum(float v, float* red) {  // fixed order
   v = group_sum<32>(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  return group_sum<32>(red[threadIdx.x & 31]);
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) t += red[i];
+  return t;
 }
 
-// one block per (image, group): joins the slabs and the group's channels. A thread takes every `parts`-th
-// slab of one channel (parts = kJoin / P, one where the group is wider), the first eight from registers in
-// the second round.
-__global__ void __launch_bounds__(kJoin) gn_stats_join_kernel(const float2* __restrict__ part, GnShape g, float eps,
-                                                              float2* __restrict__ stat, float* __restrict__ mean,
-                                                              float* __restrict__ rstd) {
+// The forward joins the channels of a group already in the slabs' blocks: one part a slab is left of a group, where
+// a part a channel made the join long for wide groups and many images (3 x 36992 x 584 with one group 106 -> 93 us,
+// 32 x 4096 x 512 with 32 groups 100 -> 86; images of a few groups' channels 0 to 1 us slower). The backward keeps
+// its parts by channel: dw and db need them.
+// one block per (image, group): joins the slabs (and the column tiles that the group crosses); a thread keeps its
+// first eight parts in registers for the second round
+__global__ void __launch_bounds__(kJoinFwd) gn_stats_join_kernel(const float2* __restrict__ part, GnShape g, int width,
+                                                              float eps, float2* __restrict__ stat,
+                                                              float* __restrict__ mean, float* __restrict__ rstd) {
   constexpr int kHeld = 8;
-  __shared__ float red[kJoin / 32];
+  __shared__ float red[kJoinFwd / 32];
   const int n = blockIdx.x / g.G, gr = blockIdx.x % g.G;
-  const float2* base = part + (int64_t)n * g.chunks * g.C + (int64_t)gr * g.P;
-  const int parts = g.P < kJoin ? kJoin / g.P : 1;
-  const int c0 = g.P < kJoin ? (int)threadIdx.x % g.P : (int)threadIdx.x;
-  const int k0 = g.P < kJoin ? (int)threadIdx.x / g.P : 0;
-  auto count = [&](int k) {
-    const int64_t r0 = (int64_t)k * g.rows;
-    return (float)(g.S - r0 < g.rows ? g.S - r0 : g.rows);
+  const int c0 = gr * g.P, t0 = c0 / width, segs = (c0 + g.P - 1) / width - t0 + 1;  // width: channels of a tile
+  const float2* base = part + (int64_t)n * g.chunks * (g.G + g.tiles - 1) + t0 + gr;
+  const int items = g.chunks * segs;
+  auto value = [&](int i) {
+    const int k = segs == 1 ? i : i / segs;
+    return base[(int64_t)k * (g.G + g.tiles - 1) + (segs == 1 ? 0 : i - k * segs)];
   };
-  const bool mine = k0 < parts;
+  auto count = [&](int i) {  // values behind part i
+    const int k = segs == 1 ? i : i / segs;
+    const int64_t left = g.S - (int64_t)k * g.rows;
+    const float rows = (float)(left < g.rows ? left : g.rows);
+    if (segs == 1) return rows * (float)g.P;
+    const int lo = (t0 + i - k * segs) * width, a = c0 > lo ? c0 : lo, b = c0 + g.P < lo + width ? c0 + g.P : lo + width;
+    return rows * (float)(b - a);
+  };
   pdl_launch_dependents();
   pdl_wait();
   float2 v[kHeld];
   float t = 0.0f, q = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int k = k0 + i * parts;
-    v[i] = mine && c0 < g.P && k < g.chunks ? base[(int64_t)k * g.C + c0] : make_float2(0.0f, 0.0f);
+  for (int j = 0; j < kHeld; ++j) {
+    const int i = threadIdx.x + j * kJoinFwd;
+    v[j] = i < items ? value(i) : make_float2(0.0f, 0.0f);
   }
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (k0 + i * parts < g.chunks) t = fmaf(count(k0 + i * parts), v[i].x, t);
-  auto rest = [&](auto f) {  // what is not held in v
-    if (mine)
-      for (int c = c0; c < g.P; c += kJoin)
-#pragma unroll 4
-        for (int k = k0 + (c == c0 ? kHeld * parts : 0); k < g.chunks; k += parts) f(count(k), base[(int64_t)k * g.C + c]);
-  };
-  rest([&](float n_, float2 u) { t = fmaf(n_, u.x, t); });
+  for (int j = 0; j < kHeld; ++j)
+    if (threadIdx.x + j * kJoinFwd < items) t = fmaf(count(threadIdx.x + j * kJoinFwd), v[j].x, t);
+  for (int i = threadIdx.x + kHeld * kJoinFwd; i < items; i += kJoinFwd) t = fmaf(count(i), value(i).x, t);
   const float total = (float)((double)g.S * g.P);
-  const float mu = block_sum(t, red) / total;
+  const float mu = block_sum<kJoinFwd>(t, red) / total;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (mine && c0 < g.P && k0 + i * parts < g.chunks) q += fmaf(count(k0 + i * parts) * (v[i].x - mu), v[i].x - mu, v[i].y);
-  rest([&](float n_, float2 u) { q += fmaf(n_ * (u.x - mu), u.x - mu, u.y); });
-  const float var = block_sum(q, red) / total;
+  for (int j = 0; j < kHeld; ++j)
+    if (threadIdx.x + j * kJoinFwd < items) q += fmaf(count(threadIdx.x + j * kJoinFwd) * (v[j].x - mu), v[j].x - mu, v[j].y);
+  for (int i = threadIdx.x + kHeld * kJoinFwd; i < items; i += kJoinFwd) {
+    const float2 u = value(i);
+    q += fmaf(count(i) * (u.x - mu), u.x - mu, u.y);
+  }
+  const float var = block_sum<kJoinFwd>(q, red) / total;
   if (threadIdx.x == 0) {
     const float s = 1.0f / sqrtf(var + eps);
     stat[blockIdx.x] = make_float2(mu, s);
@@ -493,8 +531,8 @@ __global__ void __launch_bounds__(kJoin) gn_bwd_join_kernel(const float2* __rest
     __syncthreads();
   }
   const float inv = 1.0f / (float)((double)g.S * g.P);
-  m1 = block_sum(m1, red) * inv;
-  m2 = block_sum(m2, red) * inv;
+  m1 = block_sum<kJoin>(m1, red) * inv;
+  m2 = block_sum<kJoin>(m2, red) * inv;
   if (threadIdx.x == 0) stat[blockIdx.x] = make_float2(m1, m2);
 }
 
@@ -1165,7 +1203,7 @@ extern "C" size_t gn_groupnorm_fwd_workspace(int64_t N, int64_t S, int64_t C, in
   int vpt = 0;
   if (plan_resident(N, S, C, G, (int)dt_size(dt), kFwdMost, &vpt).cs) return 0;
   const GnShape g = plan(N, S, C, G, (int)dt_size(dt), true);
-  return up16((size_t)N * g.G * 8) + (size_t)N * g.chunks * g.C * 8;
+  return up16((size_t)N * g.G * 8) + (size_t)N * g.chunks * (g.G + g.tiles - 1) * 8;
 }
 
 extern "C" gn_status gn_groupnorm_fwd(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
@@ -1196,8 +1234,9 @@ extern "C" gn_status gn_groupnorm_fwd(const void* x, const void* w, const void* 
   gn_status st = launch(dt == GN_BF16 ? (void*)gn_stats_kernel<__nv_bfloat16> : (void*)gn_stats_kernel<float>, blocks, args0,
                         s, false);
   if (st != GN_OK) return st;
-  void* args1[] = {&part, &g, &eps, &stat, &mean, &rstd};
-  st = launch((void*)gn_stats_join_kernel, N * G, args1, s, true, kJoin);
+  int width = g.tv * (int)(16 / es);
+  void* args1[] = {&part, &g, &width, &eps, &stat, &mean, &rstd};
+  st = launch((void*)gn_stats_join_kernel, N * G, args1, s, true, kJoinFwd);
   if (st != GN_OK) return st;
   void* args2[] = {&x, &ld_x, &w, &b, &stat, &g, &y, &ld_y};
   return launch(dt == GN_BF16 ? pick_apply<__nv_bfloat16>(epi) : pick_apply<float>(epi), blocks, args2, s, true);
