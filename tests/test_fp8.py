@@ -248,6 +248,26 @@ def test_padding_is_left_alone(gpu):
     assert (q[5] == 0x55).all() and (q[:5, 77:] == 0x55).all() and (s[5] == 7).all() and (s[:5, 1:] == 7).all()
 
 
+def far_rows(t, ld):
+    """t on rows `ld` elements apart"""
+    base = torch.empty(t.shape[0] * ld, dtype=torch.uint8 if t.dtype == F8 else t.dtype, device="cuda")
+    v = base.as_strided(t.shape, (ld, 1))
+    v.copy_(t.view(torch.uint8) if t.dtype == F8 else t)
+    return base.view(F8).as_strided(t.shape, (ld, 1)) if t.dtype == F8 else v
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hidden", [384, 5120])
+def test_quantiser_offsets_past_32_bits(gpu, hidden):
+    x = torch.randn(2200, hidden, device="cuda").bfloat16()
+    far = far_rows(x, 1 << 20)
+    for f in (lambda v: gn.norm_quant_fp8(v, norm="ln"), lambda v: gn.norm_quant_fp8(v[2100:], norm="rms"), lambda v: gn.quant_fp8(v, transposed=True),
+              lambda v: gn.quant_fp8(v, tile=True, transposed=True), lambda v: gn.act_grad_quant_fp8(v, v)):
+        for a, b in zip(f(x), f(far)):
+            assert a is None and b is None or (same_codes(a, b) if a.dtype == F8 else torch.equal(a, b))
+    assert gpu.device_error() == 0
+
+
 # ---------------------------------------------------------------- the product
 
 def operands(M, N, K, b_rows, seed=0):
@@ -339,6 +359,16 @@ def test_linear_strides_and_neighbours(gpu):
     assert torch.equal(out, gn.linear_fp8(aq, sa, bq, sb, d))
     big[2:M + 2, 8:8 + N] = 9.0
     assert (big == 9).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,ld", [(40, 520, 640, 1 << 26), (3000, 2000, 640, 1 << 20)])
+def test_linear_offsets_past_32_bits(gpu, M, N, K, ld):
+    aq, sa, bq, sb, d = operands(M, N, K, 128)
+    y = gn.linear_fp8(aq, sa, bq, sb, d)
+    far = torch.empty(M * ld, dtype=torch.bfloat16, device="cuda").as_strided((M, N), (ld, 1))
+    assert torch.equal(gn.linear_fp8(far_rows(aq, ld), far_rows(sa, ld), bq, sb, d, out=far), y)
+    assert gpu.device_error() == 0
 
 
 @pytest.mark.gpu
@@ -482,3 +512,15 @@ def test_helper_refusals(monkeypatch):
               lambda: gn.linear_fp8(a, sa, b, sb, out=torch.zeros(4, 64), out_dtype=torch.bfloat16)):
         with pytest.raises((ValueError, TypeError)):
             f()
+
+
+def test_stream_of_another_device_is_refused():
+    class Tensor:
+        is_cuda, device = True, torch.device("cuda", 1)
+
+    class Stream:
+        device = torch.device("cuda", 0)
+
+    for f in (gn.groupnorm_fwd, gn.groupnorm_bwd, gn.norm_quant_fp8, gn.linear_fp8):
+        with pytest.raises(ValueError, match="the stream is on"):
+            f(Tensor(), stream=Stream())

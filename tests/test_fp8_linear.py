@@ -193,3 +193,6 @@ def test_helper_refusals(monkeypatch):
         fl.backward(x, w, x, x, norm="group")
     with pytest.raises(ValueError, match="norm weight"):
         fl.backward(x, w, x, x, norm="rms")
+    w = fl.Weight(torch.zeros(1), torch.zeros(1), None, None)
+    with pytest.raises(ValueError, match="M, K"):
+        fl.forward(torch.zeros(2, 4, 8), w)

@@ -152,6 +152,43 @@ def test_in_place_and_unsaved(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,S,C,G,dt", [(2, 200, 96, 6, "bf16"), (2, 5000, 512, 32, "bf16"), (1, 9001, 264, 3, "f32")])
+def test_outputs_over_their_inputs(gpu, N, S, C, G, dt):
+    """y over x and dx over dy, on images kept on chip and on images read twice: the same bits as apart."""
+    t = make(N, S, C, dt)
+    y, mean, rstd = gn.groupnorm_fwd(t["x"], G, t["w"], t["b"], epilogue="silu")
+    x = t["x"].clone()
+    gn.groupnorm_fwd(x, G, t["w"], t["b"], epilogue="silu", out=x)
+    assert torch.equal(x, y)
+    dx, dw, db = gn.groupnorm_bwd(t["x"], G, t["w"], t["b"], mean, rstd, t["dy"], epilogue="silu")
+    code = gn.GN_BF16 if dt == "bf16" else gn.GN_F32
+    n = gn.gn_groupnorm_bwd_workspace(N, S, C, G, code)
+    ws, dw2, db2, dy = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(dw), torch.empty_like(db), t["dy"].clone()
+    gn.check(gn.gn_groupnorm_bwd(t["x"].data_ptr(), t["w"].data_ptr(), t["b"].data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                 dy.data_ptr(), dy.data_ptr(), dw2.data_ptr(), db2.data_ptr(), ws.data_ptr(), n, N, S, C, G, C, C, C,
+                                 gn.GN_EPI_SILU, code, torch.cuda.current_stream().cuda_stream))
+    assert torch.equal(dy, dx) and torch.equal(dw2, dw) and torch.equal(db2, db)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [512, 2048])
+def test_offsets_past_32_bits(gpu, C):
+    """Rows so far apart that the last ones lie beyond 2^31 elements (images kept on chip; read twice)."""
+    S, ld = 2200, 1 << 20
+    t = make(1, S, C, "bf16")
+    y, mean, rstd = gn.groupnorm_fwd(t["x"], 32, t["w"], t["b"], epilogue="silu")
+    dx, dw, db = gn.groupnorm_bwd(t["x"], 32, t["w"], t["b"], mean, rstd, t["dy"], epilogue="silu")
+    far = [torch.empty(S * ld, dtype=torch.bfloat16, device="cuda").as_strided((1, S, C), (S * ld, ld, 1)) for _ in range(3)]
+    far[0].copy_(t["x"])
+    far[1].copy_(t["dy"])
+    y2, mean2, rstd2 = gn.groupnorm_fwd(far[0], 32, t["w"], t["b"], epilogue="silu", out=far[2])
+    assert torch.equal(y2, y) and torch.equal(mean2, mean) and torch.equal(rstd2, rstd)
+    dx2, dw2, db2 = gn.groupnorm_bwd(far[0], 32, t["w"], t["b"], mean, rstd, far[1], epilogue="silu")
+    assert torch.equal(dx2, dx) and torch.equal(dw2, dw) and torch.equal(db2, db)
+    assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
 def test_padding_is_left_alone(gpu):
     """Bytes between the rows of a padded output, and rows behind the last image, keep what they held."""
     x = torch.randn(2, 9, 36, device="cuda").bfloat16()
