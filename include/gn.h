@@ -327,7 +327,7 @@ gn_status gn_act_fwd(const void* z, void* y, int64_t n, gn_epilogue epi, gn_dtyp
  * 16 bytes; any C, G dividing C. y may alias x when ld_y == ld_x (in place).
  * ws: device scratch of gn_groupnorm_fwd_workspace(N, S, C, G, dt) bytes, 16-byte aligned, owned by
  * the caller, contents ignored on entry; calls that overlap on the GPU need one each. The size is
- * that of the current device. Every sum runs in a fixed order: the same bits on every run.
+ * that of the current device; 0 for images that stay on chip: ws may then be NULL. Every sum runs in a fixed order: the same bits on every run.
  * N == 0 or S == 0: nothing is launched and no statistic is written.
  * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE (sizes, G not dividing C, strides), GN_ERR_NULL, GN_ERR_ALIGN,
  * GN_ERR_WORKSPACE, GN_ERR_CUDA. */
@@ -380,7 +380,7 @@ gn_status gn_norm_quant_fp8(const void* x, const void* g, const void* beta, void
  *                transpose, qt the transpose of q (a weight; dy must be NULL)
  * q or qt may be NULL (not written). db: fp32 [cols], may be NULL: the column sums of v (a bias
  * gradient; fp32 in a fixed order), which needs ws of gn_quant_fp8_workspace(rows, cols) bytes, 16-byte
- * aligned, contents ignored. rows <= 8388480.
+ * aligned, contents ignored. rows <= 8388480, fewer than 2^31 blocks of 128 x 128.
  * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE, GN_ERR_UNSUPPORTED (an epilogue without dy; dy with tiles),
  * GN_ERR_NULL, GN_ERR_ALIGN, GN_ERR_WORKSPACE, GN_ERR_CUDA. rows == 0: nothing is launched, db is
  * set to zero. */
@@ -399,7 +399,7 @@ gn_status gn_quant_fp8(const void* x, const void* dy, void* q, float* scale, voi
  * fp32. The gradients of the layer are the same product on gn_quant_fp8's operands: dx = dz W
  * (A = dz by rows, B = W transposed), dW = dz^T x (A = dz transposed, B = x transposed, b_rows 1).
  * Any M, N, K >= 1; A, B, y, d 16-byte aligned, row strides ld_a, ld_b, ld_y of whole 16 bytes.
- * M <= 8388480.
+ * M, N <= 8388480, K <= 2^31 - 129.
  * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE, GN_ERR_UNSUPPORTED (activation with GN_F32, accumulate with
  * GN_BF16), GN_ERR_NULL, GN_ERR_ALIGN, GN_ERR_CUDA. M == 0 or N == 0: nothing is launched. */
 gn_status gn_linear_fp8(const void* A, const float* sa, const void* B, const float* sb, const float* d,

