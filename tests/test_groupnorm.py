@@ -98,7 +98,7 @@ def check(t, G, dt, act, eps=1e-5, w=True, b=True, shape=None):
 # group; as many groups as channels; widths that end inside a vector; many small images; long images
 SHAPES = [(1, 1, 64, 8), (2, 1, 8, 8), (1, 63, 320, 32), (3, 17, 30, 3), (2, 50, 40, 1), (2, 33, 24, 24), (2, 65, 77, 7),
           (33, 5, 64, 4), (1, 4099, 128, 32), (2, 1031, 640, 32), (1, 300, 1536, 16), (1, 20000, 64, 32), (2, 4096, 640, 32), (1, 70000, 64, 4), (2, 30001, 48, 3), (1, 9000, 520, 1),
-          (1, 17, 8192, 2), (1, 40, 4104, 27), (300, 7, 32, 2)]
+          (1, 17, 8192, 2), (1, 40, 4104, 27), (300, 7, 32, 2), (3, 2500, 1032, 2)]
 
 
 @pytest.mark.gpu
