@@ -19,6 +19,7 @@
 //     has to read, and for outputs of few tiles.
 // Every mbarrier wait is bounded; a timeout records the error bit, and the CTA leaves its loops, waits
 // for its own tensor-core work and copies, frees its tensor memory and exits.
+#include "act_pairs.cuh"
 #include "gn_common.cuh"
 #include "gn_host.h"
 #include "tcgen05.cuh"
@@ -139,13 +140,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
-// the activation of bf16 outputs: the hardware tanh, the approximate exponential and divide
+// the activation of bf16 outputs, two values at a time: the hardware tanh, exponential and reciprocal
 template <int EPI>
-__device__ __forceinline__ float f8_act(float z) {
-  if constexpr (EPI == EPI_SILU)
-    return __fdividef(z, 1.0f + __expf(-z));
-  else
-    return epi_fwd<EPI, true>(z);
+__device__ __forceinline__ float2 f8_act(float2 z) {
+  if constexpr (EPI == EPI_GELU_TANH) {
+    const float2 u = mul2(z, fma2(mul2(z, z), dup2(kGeluK * kGeluC), dup2(kGeluK))), h = mul2(z, dup2(0.5f));
+    return fma2(h, make_float2(tanh_f<true>(u.x), tanh_f<true>(u.y)), h);
+  } else {
+    return act_pair<EPI, true>(z);
+  }
 }
 
 // ---------------------------------------------------------------- pairs of SMs
@@ -429,50 +432,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int b = 0; b < 128 / kCols; ++b) {
         const int col0 = nh + b * kCols;
         if (col0 < a.N) {  // uniform over the warp
-          if (box_used) {  // the box's previous store has finished reading it
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
-          }
+          // (the values first, so that the wait for the box passes meanwhile)
+          auto box_free = [&] {  // the box's previous store has finished reading it
+            if (box_used) {
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+            }
+          };
           auto bias = [&](int n) { return a.d && n < a.N ? __ldg(a.d + n) : 0.0f; };
           auto bias4 = [&](int n) {
             if (a.d && n + 4 <= a.N) return __ldg(reinterpret_cast<const float4*>(a.d + n));
             return make_float4(bias(n), bias(n + 1), bias(n + 2), bias(n + 3));
           };
           if constexpr (BROW) {
+            float2 o[kCols / 8][4];
 #pragma unroll
             for (int jj = 0; jj < kCols / 8; ++jj) {
-              const int c = 8 * jj + 2 * (lane & 3);  // column of the box
-              const float d0 = bias(col0 + c), d1 = bias(col0 + c + 1);
+              const int c = col0 + 8 * jj + 2 * (lane & 3);
+              const float2 d = make_float2(bias(c), bias(c + 1));
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int cb = b * kCols + 8 * jj;  // column of the half
-                const float2 v = acc[32 * (i >> 1) + 16 * (cb >> 6) + 2 * ((cb & 63) >> 3) + (i & 1)];
+                o[jj][i] = f8_act<EPI>(add2(acc[32 * (i >> 1) + 16 * (cb >> 6) + 2 * ((cb & 63) >> 3) + (i & 1)], d));
+              }
+            }
+            box_free();
+#pragma unroll
+            for (int jj = 0; jj < kCols / 8; ++jj) {
+              const int c = 8 * jj + 2 * (lane & 3);  // column of the box
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
                 const int r = (lane >> 2) + 8 * i;
-                const float o0 = f8_act<EPI>(v.x + d0), o1 = f8_act<EPI>(v.y + d1);
                 constexpr int kEs = F32 ? 4 : 2;
                 uint8_t* at = box + r * 128 + ((((c * kEs) >> 4) ^ (r & 7)) << 4) + ((c * kEs) & 15);
-                if constexpr (F32) *reinterpret_cast<float2*>(at) = make_float2(o0, o1);
-                else *reinterpret_cast<uint32_t*>(at) = Vec<__nv_bfloat16>::join(o0, o1);
+                if constexpr (F32) *reinterpret_cast<float2*>(at) = o[jj][i];
+                else *reinterpret_cast<uint32_t*>(at) = Vec<__nv_bfloat16>::join(o[jj][i].x, o[jj][i].y);
               }
             }
           } else {
             uint8_t* row = box + lane * 128;
+            uint4 w[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               constexpr int kE = kCols / 8;  // elements of a 16-byte chunk
               float o[kE];
 #pragma unroll
               for (int e = 0; e < kE; e += 4) {
-                const float2 u = acc[(b * kCols + c * kE + e) / 2], v = acc[(b * kCols + c * kE + e) / 2 + 1];
                 const float4 d = bias4(col0 + c * kE + e);
-                o[e] = f8_act<EPI>(u.x + d.x), o[e + 1] = f8_act<EPI>(u.y + d.y);
-                o[e + 2] = f8_act<EPI>(v.x + d.z), o[e + 3] = f8_act<EPI>(v.y + d.w);
+                const float2 u = f8_act<EPI>(add2(acc[(b * kCols + c * kE + e) / 2], make_float2(d.x, d.y)));
+                const float2 v = f8_act<EPI>(add2(acc[(b * kCols + c * kE + e) / 2 + 1], make_float2(d.z, d.w)));
+                o[e] = u.x, o[e + 1] = u.y, o[e + 2] = v.x, o[e + 3] = v.y;
               }
-              uint4 w;
-              if constexpr (F32) w = Vec<float>::pack(o);
-              else w = Vec<__nv_bfloat16>::pack(o);
-              *reinterpret_cast<uint4*>(row + ((c ^ (lane & 7)) << 4)) = w;
+              if constexpr (F32) w[c] = Vec<float>::pack(o);
+              else w[c] = Vec<__nv_bfloat16>::pack(o);
             }
+            box_free();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(row + ((c ^ (lane & 7)) << 4)) = w[c];
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
@@ -550,7 +566,10 @@ __device__ __forceinline__ void add_totals(const Fp8Args& a, const float* total,
       for (int j = 0; j < CS; ++j)
         if (j < cs) z[0] += v[u][j].x, z[1] += v[u][j].y, z[2] += v[u][j].z, z[3] += v[u][j].w;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[e] = f8_act<EPI>(z[e] + d[e]);
+      for (int e = 0; e < 4; e += 2) {
+        const float2 o = f8_act<EPI>(make_float2(z[e] + d[e], z[e + 1] + d[e + 1]));
+        z[e] = o.x, z[e + 1] = o.y;
+      }
       const int64_t at = (int64_t)(m0 + i + 4 * u) * a.ldy + n;
       if constexpr (F32) {
         float* p = static_cast<float*>(a.y) + at;
