@@ -378,9 +378,10 @@ gn_status gn_norm_quant_fp8(const void* x, const void* g, const void* beta, void
  *                qt [cols, rows] in blocks of 128 along the rows of v, scale_t [cols, ceil(rows / 128)]
  *   GN_FP8_TILE: blocks of 128 x 128; scale [ceil(rows / 128), ceil(cols / 128)], scale_t its
  *                transpose, qt the transpose of q (a weight; dy must be NULL)
- * q or qt may be NULL (not written). db: fp32 [cols], may be NULL: the column sums of v (a bias
- * gradient; fp32 in a fixed order), which needs ws of gn_quant_fp8_workspace(rows, cols) bytes, 16-byte
- * aligned, contents ignored. rows <= 8388480, fewer than 2^31 blocks of 128 x 128.
+ * q or qt may be NULL (not written). db: fp32 [cols], may be NULL: the column sums of v, with dy (a bias
+ * gradient) or without (those of x, tiles included); fp32 in a fixed order. It needs ws of
+ * gn_quant_fp8_workspace(rows, cols) bytes, 16-byte aligned, contents ignored. rows <= 8388480, fewer
+ * than 2^31 blocks of 128 x 128.
  * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE, GN_ERR_UNSUPPORTED (an epilogue without dy; dy with tiles),
  * GN_ERR_NULL, GN_ERR_ALIGN, GN_ERR_WORKSPACE, GN_ERR_CUDA. rows == 0: nothing is launched, db is
  * set to zero. */

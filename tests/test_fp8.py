@@ -203,6 +203,38 @@ def test_activation_gradient(gpu, rows, cols, dt, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", MATS)
+def test_column_sums_of_a_matrix_as_it_is(gpu, rows, cols, dt, tile):
+    """db without dy: the column sums of x itself, next to the codes that x has without them. Sums of up to 1031
+    fp32 terms, slab by slab: 4e-6 of the magnitudes, as for the gradient."""
+    g = torch.Generator().manual_seed(rows + cols)
+    x = padded(torch.randn(rows, cols, generator=g), DT[dt], extra=16)
+    want = gn.quant_fp8(x, tile=tile, transposed=True)
+    r, c = (blocks(rows), blocks(cols)) if tile else (rows, cols)
+    ldq, ldqt = (cols + 15) // 16 * 16, (rows + 15) // 16 * 16
+    code = gn.GN_BF16 if dt == "bf16" else gn.GN_F32
+    n = gn.gn_quant_fp8_workspace(rows, cols)
+    for by_rows, transposed in ((True, True), (True, False), (False, True)):
+        q, qt = (torch.zeros(a, b, dtype=torch.uint8, device="cuda") for a, b in ((rows, ldq), (cols, ldqt)))
+        s, st = torch.zeros(r, blocks(cols), device="cuda"), torch.zeros(c, blocks(rows), device="cuda")
+        ws = torch.full((n // 4,), float("nan"), device="cuda")
+        db = torch.full((cols,), 7.0, device="cuda")
+        gn.check(gn.gn_quant_fp8(x.data_ptr(), None, q.data_ptr() if by_rows else None, s.data_ptr(), qt.data_ptr() if transposed else None,
+                                 st.data_ptr(), db.data_ptr(), ws.data_ptr(), n, rows, cols, x.stride(0) if rows > 1 else ldq, 0, ldq,
+                                 blocks(cols), ldqt, blocks(rows), gn.GN_FP8_TILE if tile else gn.GN_FP8_VEC, 0, code,
+                                 torch.cuda.current_stream().cuda_stream))
+        X = x.double()
+        assert ((db.double() - X.sum(0)).abs() <= 4e-6 * X.abs().sum(0)).all()
+        if by_rows:
+            assert same_codes(q.view(F8)[:, :cols], want[0]) and torch.equal(s, want[1])
+        if transposed:
+            assert same_codes(qt.view(F8)[:, :rows], want[2]) and torch.equal(st, want[3])
+    assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_special_values(gpu, dt):
     """Zero blocks, the smallest and largest magnitudes, NaN and infinities: only their own blocks see them."""

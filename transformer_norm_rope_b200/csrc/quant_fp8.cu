@@ -720,10 +720,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) quant_tile_kernel(const Quant
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) red_max[0][warp] = m;
-      } else if (lane < L) {
+      }
+      if ((GRAD || !TILE) && lane < L) {
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
-          *reinterpret_cast<float4*>(&red_max[warp][lv * E + e]) = make_float4(cmax[e], cmax[e + 1], cmax[e + 2], cmax[e + 3]);
+          if constexpr (!TILE)
+            *reinterpret_cast<float4*>(&red_max[warp][lv * E + e]) = make_float4(cmax[e], cmax[e + 1], cmax[e + 2], cmax[e + 3]);
           if constexpr (GRAD)
             *reinterpret_cast<float4*>(&red_sum[warp][lv * E + e]) = make_float4(csum[e], csum[e + 1], csum[e + 2], csum[e + 3]);
         }
@@ -882,6 +884,7 @@ void* pick_norm(int norm, int epi, int shape) {
 template <typename T>
 void* pick_tile(int epi, bool grad, bool tile) {
   if (!grad) return tile ? (void*)quant_tile_kernel<T, EPI_NONE, false, true> : (void*)quant_tile_kernel<T, EPI_NONE, false, false>;
+  if (tile) return (void*)quant_tile_kernel<T, EPI_NONE, true, true>;
   return epi == GN_EPI_GELU_TANH ? (void*)quant_tile_kernel<T, EPI_GELU_TANH, true, false>
          : epi == GN_EPI_SILU    ? (void*)quant_tile_kernel<T, EPI_SILU, true, false>
                                  : (void*)quant_tile_kernel<T, EPI_NONE, true, false>;
@@ -979,6 +982,8 @@ extern "C" gn_status gn_quant_fp8(const void* x, const void* dy, void* q, float*
   if ((q && (!aligned16(q) || ld_q % 16)) || (qt && (!aligned16(qt) || ld_qt % 16))) return GN_ERR_ALIGN;
   if (db && (!ws || ws_bytes < gn_quant_fp8_workspace(rows, cols))) return GN_ERR_WORKSPACE;
   if (db && !aligned16(ws)) return GN_ERR_ALIGN;
+  // only the gradient's kernels form column sums: those of a matrix as it is go through them as dy * 1
+  if (db && !dy) dy = x, ld_dy = ld_x;
   QuantArgs a{x, dy, static_cast<uint8_t*>(q), scale, static_cast<uint8_t*>(qt), scale_t,
               db ? static_cast<float*>(ws) : nullptr, rows, cols, ld_x, ld_dy, ld_q, ld_s, ld_qt, ld_st,
               (unsigned)blocks_of(rows), (unsigned)blocks_of(cols)};
