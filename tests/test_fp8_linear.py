@@ -196,3 +196,61 @@ def test_helper_refusals(monkeypatch):
     w = fl.Weight(torch.zeros(1), torch.zeros(1), None, None)
     with pytest.raises(ValueError, match="M, K"):
         fl.forward(torch.zeros(2, 4, 8), w)
+
+
+class OfDevice1(torch.Tensor):
+    """A CPU tensor that says it lives on the second GPU."""
+
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda", 1))
+
+
+class TwoGpus:
+    """torch with two devices that only remember which of them is current; outputs are made on the CPU."""
+
+    def __init__(self):
+        self.current, outer = 0, self
+
+        class device:
+            def __init__(self, d):
+                self.d = d.index
+
+            def __enter__(self):
+                self.before, outer.current = outer.current, self.d
+
+            def __exit__(self, *exc):
+                outer.current = self.before
+
+        self.cuda = type("cuda", (), {"current_device": staticmethod(lambda: outer.current), "device": device})
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+    def empty(self, *shape, device=None, **kw):
+        return torch.empty(*shape, **kw).as_subclass(OfDevice1)
+
+    def empty_strided(self, *shape, device=None, **kw):
+        return torch.empty_strided(*shape, **kw).as_subclass(OfDevice1)
+
+
+@pytest.mark.parametrize("norm", ["none", "ln", "rms"])
+def test_every_call_runs_on_the_tensors_device(monkeypatch, norm):
+    """x on the second device while the first is current: every launch of the layer, forward and backward, goes to
+    the second one's current stream (the streams' handles stand for their devices here)."""
+    gpus, calls = TwoGpus(), []
+    monkeypatch.setattr(gn, "_TORCH", gpus)
+    monkeypatch.setattr(gn, "_WORKSPACE", {})
+    monkeypatch.setattr(gn, "_stream", lambda stream=None: gpus.current)
+    for f in gn.SIGNATURES:
+        if gn.SIGNATURES[f][0] is gn._st:
+            monkeypatch.setattr(gn, f, lambda *a, f=f: calls.append((f, a[-1], gpus.current)) or gn.GN_OK)
+        elif f.endswith("_workspace"):
+            monkeypatch.setattr(gn, f, lambda *a: 16)
+    M, N, K = 32, 64, 128
+    t = {k: torch.zeros(s, dtype=torch.bfloat16).as_subclass(OfDevice1) for k, s in dict(x=(M, K), W=(N, K), g=(K,), beta=(K,), dy=(M, N)).items()}
+    args = dict(norm=norm, g=None if norm == "none" else t["g"], beta=t["beta"] if norm == "ln" else None, act="silu")
+    w = fl.prepare(t["W"])
+    y, mean, rstd, z = fl.forward_keeping_z(t["x"], w, **args)
+    fl.backward(t["x"], w, z, t["dy"], mean=mean, rstd=rstd, **args)
+    assert gpus.current == 0 and {"gn_act_fwd", "gn_linear_fp8", "gn_quant_fp8"} <= {c[0] for c in calls}
+    assert all(stream == 1 and current == 1 for _, stream, current in calls), [c for c in calls if c[1:] != (1, 1)]

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import inspect
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -233,6 +234,24 @@ def empty_rows(shape, dtype, device):
     return base.as_strided(shape, strides)
 
 
+def _on_its_device(f):
+    """Runs a helper with its first tensor's device current, whose current stream it then uses; an explicit
+    stream and where outputs are allocated are left as they are."""
+    name = next(iter(inspect.signature(f).parameters))
+
+    @functools.wraps(f)
+    def call(*args, **kwargs):
+        x = args[0] if args else kwargs.get(name)
+        cuda = _torch().cuda
+        if not getattr(x, "is_cuda", False) or x.device.index == cuda.current_device():
+            return f(*args, **kwargs)
+        with cuda.device(x.device):
+            return f(*args, **kwargs)
+
+    return call
+
+
+@_on_its_device
 def rmsnorm_fwd(x, w, eps=1e-6, gemma=False, epilogue="none", out=None, save_stats=True, stream=None):
     """y = epi(x * rsqrt(mean(x^2) + eps) * w') -> (y, inv_rms[rows] fp32 or None)."""
     torch = _torch()
@@ -247,6 +266,7 @@ def rmsnorm_fwd(x, w, eps=1e-6, gemma=False, epilogue="none", out=None, save_sta
     return y, r
 
 
+@_on_its_device
 def rmsnorm_bwd(x, w, inv_rms, dy, gemma=False, epilogue="none", want_dw=True, stream=None):
     """-> (dx, dw fp32 or None)."""
     torch = _torch()
@@ -266,6 +286,7 @@ def rmsnorm_bwd(x, w, inv_rms, dy, gemma=False, epilogue="none", want_dw=True, s
     return dx, dw
 
 
+@_on_its_device
 def layernorm_fwd(x, w=None, b=None, eps=1e-5, epilogue="none", out=None, save_stats=True, stream=None):
     """y = epi((x - mean) * rstd * w + b) -> (y, mean, rstd)."""
     torch = _torch()
@@ -282,6 +303,7 @@ def layernorm_fwd(x, w=None, b=None, eps=1e-5, epilogue="none", out=None, save_s
     return y, mu, rs
 
 
+@_on_its_device
 def layernorm_bwd(x, w, b, mean, rstd, dy, epilogue="none", want_wgrad=True, stream=None):
     """-> (dx, dw, db) (dw, db fp32 or None)."""
     torch = _torch()
@@ -434,6 +456,7 @@ def act_grad(z, dy, epilogue="silu", out=None, stream=None):
     return dz
 
 
+@_on_its_device
 def act_fwd(z, epilogue="silu", out=None, stream=None):
     """y = act(z), elementwise (contiguous; out may be z itself)."""
     _need(z, "z")
