@@ -113,6 +113,21 @@ def test_groupnorm(gpu, N, S, C, G, dt, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("C,G", [(171, 1), (77, 7), (5, 5), (4104, 27), (1, 1)])
+def test_one_position_at_any_width(gpu, C, G, dt, act):
+    """One row: a contiguous tensor whatever its width, with nothing that steps by its stride."""
+    t = make(1, 1, C, dt)
+    check(t, G, dt, act)
+    y, _, _ = gn.groupnorm_fwd(t["x"], G, t["w"], t["b"], epilogue=act)
+    out = torch.full((1, 1, C + 1), 7.0, dtype=DT[dt], device="cuda")
+    gn.groupnorm_fwd(t["x"], G, t["w"], t["b"], epilogue=act, out=out[..., :C])
+    assert torch.equal(out[..., :C], y) and (out[..., C] == 7).all()
+    assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("w,b", [(False, False), (True, False), (False, True)])
 def test_absent_parameters(gpu, w, b):
     check(make(2, 100, 96, "bf16"), 6, "bf16", "silu", w=w, b=b)
@@ -320,6 +335,21 @@ BIG = dict(S=100000, C=512, G=32, ldx=512, ldy=512)
 def test_refusals(call, kw, status):
     gn.load()
     assert call(**kw) == status
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 1, 171), (1, 1, 5), (1, 1, 64), (2, 3, 64), (2, 3, 77), (1, 1, 1), (3, 0, 77), (0, 4, 64)])
+def test_row_strides_of_inputs_and_outputs(monkeypatch, shape, dt):
+    """Every row stride that reaches the library is whole 16 bytes, an output's own where it has more than one row."""
+    monkeypatch.setattr(gn, "_on_gpu", lambda t: True)
+    x = gn.empty_rows(shape, DT[dt], "cpu")
+    es = x.element_size()
+    N, S, C, ld = gn._images(x)
+    y, ldy = gn._like_rows(x)
+    assert (N, S, C) == shape and y.shape == x.shape and y.dtype == x.dtype
+    assert ld * es % 16 == 0 and ldy * es % 16 == 0 and ldy >= C
+    if N * S > 1:
+        assert gn._images(y)[3] == ldy and y.stride(-2) == ldy
 
 
 def test_helper_refusals(monkeypatch):

@@ -616,13 +616,13 @@ def _workspace(query, name, device, *sizes):
     return (_empty((n,), (1,), _torch().uint8, device) if n else None), n
 
 
-def _like_rows(x, ld):
-    """An output of x's shape and type and its row stride: x's own layout where it is contiguous in whole 16
-    bytes, else rows that start on 16-byte boundaries."""
-    if x.is_contiguous() and ld * x.element_size() % 16 == 0:
-        return _torch().empty_like(x), x.shape[-1]
-    es = x.element_size()
-    return empty_rows(x.shape, x.dtype, x.device), (x.shape[-1] * es + 15) // 16 * 16 // es
+def _like_rows(x):
+    """An output of x's shape and type and its row stride: x's own layout where it is contiguous and its width is
+    whole 16 bytes, else rows that start on 16-byte boundaries."""
+    width, es = x.shape[-1], x.element_size()
+    if x.is_contiguous() and width * es % 16 == 0:
+        return _torch().empty_like(x), width
+    return empty_rows(x.shape, x.dtype, x.device), (width * es + 15) // 16 * 16 // es
 
 
 @_placed
@@ -636,7 +636,7 @@ def groupnorm_fwd(x, groups, w=None, b=None, eps=1e-5, epilogue="none", out=None
     _need(w, "w", like=x, shape=(Cn,), dtype=dtype, optional=True)
     _need(b, "b", like=x, shape=(Cn,), dtype=dtype, optional=True)
     if out is None:
-        y, ldy = _like_rows(x, ld)
+        y, ldy = _like_rows(x)
     else:
         y = out
         _need(y, "out", like=x, shape=x.shape, contiguous=False)
@@ -663,7 +663,7 @@ def groupnorm_bwd(x, groups, w, b, mean, rstd, dy, epilogue="none", want_wgrad=T
     _need(rstd, "rstd", like=x, shape=(N, groups), dtype=f32)
     _need(dy, "dy", like=x, shape=x.shape, contiguous=False)
     _, _, _, lddy = _images(dy, "dy", like=x, dtype=dtype)
-    dx, lddx = _like_rows(x, ld)
+    dx, lddx = _like_rows(x)
     dw = db = None
     if want_wgrad:
         dw, db = _empty((Cn,), (1,), f32, device), _empty((Cn,), (1,), f32, device)
