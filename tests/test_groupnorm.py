@@ -226,6 +226,15 @@ def test_empty(gpu, N, S):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_statistics_of_no_positions_are_nan(gpu, dt):
+    gen = torch.full((3, 4), 5.0, device="cuda")  # what the allocator hands out next is not NaN already
+    del gen
+    _, mean, rstd = gn.groupnorm_fwd(torch.zeros(3, 0, 32, device="cuda", dtype=DT[dt]), 4)
+    assert mean.shape == rstd.shape == (3, 4) and torch.isnan(mean).all() and torch.isnan(rstd).all()
+
+
+@pytest.mark.gpu
 def test_nan_stays_in_its_group(gpu):
     x = torch.randn(2, 40, 32, device="cuda")
     x[0, 3, 5] = float("nan")

@@ -629,7 +629,8 @@ def _like_rows(x):
 def groupnorm_fwd(x, groups, w=None, b=None, eps=1e-5, epilogue="none", out=None, save_stats=True, stream=None):
     """GroupNorm of channels-last images x [N, ..., C] with an activation:
     y = epi((x - mean) * rstd * w + b), statistics over each image's groups of C / groups consecutive
-    channels -> (y, mean [N, groups], rstd [N, groups]) (statistics fp32, or None)."""
+    channels -> (y, mean [N, groups], rstd [N, groups]) (statistics fp32, or None; NaN for images of no
+    positions)."""
     f32 = _torch().float32
     N, S, Cn, ld = _images(x)
     dtype, device = x.dtype, x.device
@@ -644,6 +645,9 @@ def groupnorm_fwd(x, groups, w=None, b=None, eps=1e-5, epilogue="none", out=None
     shape, strides, mu, rs = (N, groups), (groups, 1), None, None
     if save_stats:
         mu, rs = _empty(shape, strides, f32, device), _empty(shape, strides, f32, device)
+        if S == 0:  # nothing is launched; the mean of no values is NaN
+            mu.fill_(float("nan"))
+            rs.fill_(float("nan"))
     dt = _dt(x)
     ws, nws = _workspace(gn_groupnorm_fwd_workspace, "gn_fwd", device, N, S, Cn, groups, dt)
     check(gn_groupnorm_fwd(x.data_ptr(), _ptr(w), _ptr(b), y.data_ptr(), _ptr(mu), _ptr(rs), _ptr(ws), nws, N, S, Cn,
