@@ -98,6 +98,101 @@ def test_layer(gpu, M, N, K, norm, gemma, act):
     assert gpu.device_error() == 0
 
 
+def odd_layer(M, N, K, seed=0):
+    """layer() with x and W on rows of whole 16 bytes, at any width"""
+    t = layer(M, N, K, seed)
+    return {k: gn.empty_rows(v.shape, v.dtype, v.device).copy_(v) if k in ("x", "W") else v for k, v in t.items()}
+
+
+def check_gradients(t, w, z, dy, mean, rstd, grads, norm, gemma, act):
+    """The layer's gradients against the same formulas in 64 bits on the codes that the layer itself makes of dz and of
+    the normalised rows (what those codes are of is checked apart), so that only roundings are left:
+    * dW: fp32 sums, 2^-24 (M + M / 128 + 4) of the magnitudes;
+    * dxn is bf16, half a step 2^-8 of each value, and the product's sums 2^-24 (N + N / 128 + 4) of the magnitudes: e;
+    * dbeta = sum dxn, dg = sum dxn x^: e of each term, and 2e-5 of the magnitudes for the sums and for x^;
+    * dx = rstd P(dxn g') with P a projection for each row: 2-norm of rstd max|g'| e, half a step of dx, and 2e-5 of
+      rstd |dxn g'| for the evaluation. Without a norm dx is dxn.
+    A gradient of zeros must not pass: each tolerance is below half of the gradient's own 2-norm."""
+    dx, dg, dbeta, dW, dbias = grads
+    M, N = z.shape
+    q, s, qt, st, db = gn.act_grad_quant_fp8(z, dy, epilogue=act)
+    if norm == "ln":
+        xn = gn.layernorm_fwd(t["x"], t["g"], t["beta"], 1e-5)[0]
+    elif norm == "rms":
+        xn = gn.rmsnorm_fwd(t["x"], t["g"], 1e-5, gemma=gemma)[0]
+    else:
+        xn = t["x"]
+    xt, xts = gn.quant_fp8(xn, by_rows=False, transposed=True)
+
+    def holds(got, ref, tol, what, norms=False):
+        assert got.shape == ref.shape and torch.isfinite(got).all(), what
+        d = (got.double() - ref).abs()
+        assert d.norm() <= tol.norm() if norms else (d <= tol).all(), f"{what}: {d.norm():.3g} off, {tol.norm():.3g} allowed"
+        assert tol.norm() <= 0.5 * ref.norm(), f"{what}: the tolerance {tol.norm():.3g} says nothing about {ref.norm():.3g}"
+
+    a, b = values(qt, st), values(xt, xts)
+    holds(dW, a @ b.t(), 2.0 ** -24 * (M + M / 128 + 4) * (a.abs() @ b.abs().t()), "dW")
+    if dbias is not None:
+        assert torch.equal(dbias, db)
+    a, b = values(q, s), values(w.qt, w.scale_t, tile=True)
+    dxn = a @ b.t()
+    e = 2.0 ** -8 * dxn.abs() + 2.0 ** -24 * (N + N / 128 + 4) * (a.abs() @ b.abs().t())
+    if norm == "none":
+        return holds(dx, dxn, e, "dx")
+    x, g = t["x"].double(), t["g"].double() + (1 if gemma else 0)
+    mu = x.mean(1, keepdim=True) if norm == "ln" else 0
+    r = ((x - mu).square().mean(1, keepdim=True) + 1e-5) ** -0.5
+    xh, gg = (x - mu) * r, dxn * g
+    m2 = (gg * xh).mean(1, keepdim=True)
+    dx64 = r * (gg - xh * m2 - (gg.mean(1, keepdim=True) if norm == "ln" else 0))
+    holds(dx, dx64, r * g.abs().max() * e + 2.0 ** -8 * dx64.abs() + 2e-5 * r * gg.abs(), "dx", norms=True)
+    holds(dg, (dxn * xh).sum(0), ((e + 2e-5 * dxn.abs()) * xh.abs()).sum(0), "dg")
+    if norm == "ln":
+        holds(dbeta, dxn.sum(0), (e + 2e-5 * dxn.abs()).sum(0), "dbeta")
+    else:
+        assert dbeta is None
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "silu", "gelu_tanh"])
+@pytest.mark.parametrize("norm,gemma", [("none", False), ("ln", False), ("rms", True)])
+@pytest.mark.parametrize("M,N,K", [(70, 300, 264), (33, 129, 200), (300, 333, 133), (1, 300, 264), (40, 1, 72), (2, 7, 136)])
+def test_widths_that_are_not_whole_16_bytes(gpu, M, N, K, norm, gemma, act):
+    """The product pads its rows at such widths: keeping z, the backward on a contiguous gradient, and autograd."""
+    t = odd_layer(M, N, K)
+    ng, nb = (None, None) if norm == "none" else (t["g"], t["beta"] if norm == "ln" else None)
+    args = dict(norm=norm, g=ng, beta=nb, eps=1e-5, gemma=gemma, act=act)
+    w = fl.prepare(t["W"])
+    y, mean, rstd, z = fl.forward_keeping_z(t["x"], w, t["bias"], **args)
+    assert y.shape == z.shape == (M, N)
+    q, s, _, _ = gn.norm_quant_fp8(t["x"], ng, nb, 1e-5, norm=norm, gemma=gemma)
+    a, b = values(q, s), values(w.q, w.scale, tile=True)
+    z64 = a @ b.t() + t["bias"].double()
+    tol = 2.0 ** -8 * z64.abs() + 2.0 ** -24 * (K + K / 128 + 5) * (a.abs() @ b.abs().t() + t["bias"].double().abs())
+    assert ((z.double() - z64).abs() <= tol).all()
+    v = act64(z.double(), act)  # y: the activation of the z that was kept, half a step and 2^-11 |z| for its hardware tanh
+    assert ((y.double() - v).abs() <= 2.0 ** -8 * v.abs() + (2.0 ** -11 * z.double().abs() if act != "none" else 0)).all()
+
+    assert t["dy"].is_contiguous()
+    grads = fl.backward(t["x"], w, z, t["dy"], mean=mean, rstd=rstd, **args)
+    dy = gn.empty_rows((M, N), torch.bfloat16, "cuda").copy_(t["dy"])
+    if M > 1:  # one row's norms leave too few values for the 2-norms of check_gradients
+        check_gradients(t, w, z, dy, mean, rstd, grads, norm, gemma, act)
+    again = fl.backward(t["x"], w, z, dy, mean=mean, rstd=rstd, **args)
+    assert all(p is None and q is None or torch.equal(p, q) for p, q in zip(grads, again))
+
+    leaves = {k: t[k].detach().requires_grad_(True) for k in ("x", "W")}  # (clone() would pack their rows)
+    bias = t["bias"].clone().requires_grad_(True)
+    out = fl.Fp8LinearFunction.apply(leaves["x"], leaves["W"], bias, ng, nb, norm, 1e-5, gemma, act)
+    assert torch.equal(out, y)
+    out.backward(t["dy"])
+    assert torch.equal(leaves["x"].grad, grads[0]) and torch.equal(leaves["W"].grad, grads[3].bfloat16()) and torch.equal(bias.grad, grads[4])
+    leaves["x"].grad = leaves["W"].grad = None
+    fl.Fp8LinearFunction.apply(leaves["x"], leaves["W"], None, ng, nb, norm, 1e-5, gemma, act).sum().backward()  # an expanded gradient
+    assert torch.isfinite(leaves["x"].grad).all() and torch.isfinite(leaves["W"].grad).all()
+    assert gpu.device_error() == 0
+
+
 @pytest.mark.gpu
 def test_autograd_function_and_its_graph(gpu):
     """The autograd form gives the module's gradients; a second layer's captured forward and backward replay to the

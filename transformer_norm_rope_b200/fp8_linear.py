@@ -41,6 +41,27 @@ def prepare(W, training: bool = True) -> Weight:
     return Weight(*gn.quant_fp8(W, tile=True), None, None)
 
 
+def _act(z, act):
+    """act(z) in z's layout: the product pads rows whose width is not whole 16 bytes, and the elementwise kernel
+    takes the padding (whatever it holds) along."""
+    if z.is_contiguous():
+        return gn.act_fwd(z, epilogue=act)
+    y = gn._empty(z.shape, z.stride(), z.dtype, z.device)
+    flat = ((z.shape[0] - 1) * z.stride(0) + z.shape[1],)
+    gn.act_fwd(z.as_strided(flat, (1,)), epilogue=act, out=y.as_strided(flat, (1,)))
+    return y
+
+
+def _whole_rows(t):
+    """t [M, N] with its rows on 16-byte boundaries: t itself, or a copy (a gradient that autograd hands over is
+    contiguous, or expanded, whatever its width)."""
+    es = t.element_size()
+    if t.dim() != 2 or (t.stride(1) == 1 and t.data_ptr() % 16 == 0
+                        and (t.shape[0] <= 1 or (t.stride(0) >= t.shape[1] and t.stride(0) * es % 16 == 0))):
+        return t
+    return gn.empty_rows(t.shape, t.dtype, t.device).copy_(t)
+
+
 def forward(x, weight: Weight, bias=None, norm: str = "none", g=None, beta=None, eps: float = 1e-5, gemma: bool = False,
             act: str = "none"):
     """y [M, N] bf16 = act(norm(x) W^T + bias) for x [M, K] (bf16 or, without a backward, fp32; bias fp32 [N])
@@ -56,7 +77,7 @@ def forward_keeping_z(x, weight: Weight, bias=None, norm: str = "none", g=None, 
     """The same layer keeping its pre-activation for the backward -> (y, mean, rstd, z) (y is z itself when
     act is "none")."""
     z, mean, rstd = forward(x, weight, bias, norm, g, beta, eps, gemma)
-    return (z if act == "none" else gn.act_fwd(z, epilogue=act)), mean, rstd, z
+    return (z if act == "none" else _act(z, act)), mean, rstd, z
 
 
 def backward(x, weight: Weight, z, dy, norm: str = "none", g=None, beta=None, mean=None, rstd=None, eps: float = 1e-5,
@@ -70,7 +91,7 @@ def backward(x, weight: Weight, z, dy, norm: str = "none", g=None, beta=None, me
         raise ValueError(f"norm {norm!r}: 'none', 'ln' or 'rms'")
     if norm == "rms" and g is None:
         raise ValueError("the RMSNorm backward needs the norm weight g")
-    q, s, qt, st, dbias = gn.act_grad_quant_fp8(z, dy, epilogue=act, want_db=want_dbias)
+    q, s, qt, st, dbias = gn.act_grad_quant_fp8(z, _whole_rows(dy), epilogue=act, want_db=want_dbias)
     dxn = gn.linear_fp8(q, s, weight.qt, weight.scale_t)
     if norm == "ln":
         xn, _, _ = gn.layernorm_fwd(x, g, beta, eps, save_stats=False)
@@ -106,8 +127,8 @@ def _function_class():
         def backward(ctx, dy):
             x, g, beta, mean, rstd, z, qt, scale_t = ctx.saved_tensors
             norm, eps, gemma, act, w_dtype, b_dtype = ctx.cfg
-            dx, dg, dbeta, dW, dbias = backward(x, Weight(None, None, qt, scale_t), z, dy.contiguous(), norm, g, beta, mean,
-                                                rstd, eps, gemma, act, want_dbias=b_dtype is not None)
+            dx, dg, dbeta, dW, dbias = backward(x, Weight(None, None, qt, scale_t), z, dy, norm, g, beta, mean, rstd,
+                                                eps, gemma, act, want_dbias=b_dtype is not None)
 
             def cast(t, like):
                 return None if t is None or like is None else t.to(like.dtype)
