@@ -382,7 +382,7 @@ gn_status gn_norm_quant_fp8(const void* x, const void* g, const void* beta, void
  * gradient) or without (those of x, tiles included); fp32 in a fixed order. It needs ws of
  * gn_quant_fp8_workspace(rows, cols) bytes, 16-byte aligned, contents ignored. rows <= 8388480, fewer
  * than 2^31 blocks of 128 x 128.
- * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE, GN_ERR_UNSUPPORTED (an epilogue without dy; dy with tiles),
+ * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE, GN_ERR_UNSUPPORTED (rows with an epilogue but no dy; dy with tiles),
  * GN_ERR_NULL, GN_ERR_ALIGN, GN_ERR_WORKSPACE, GN_ERR_CUDA. rows == 0: nothing is launched, db is
  * set to zero. */
 size_t gn_quant_fp8_workspace(int64_t rows, int64_t cols);

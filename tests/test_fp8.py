@@ -529,6 +529,23 @@ def test_refusals(call, kw, status):
     assert call(**kw) == status
 
 
+def test_gradient_of_no_rows():
+    """dy of an empty tensor is a null pointer: an activation asks for dy only where there are rows."""
+    gn.load()
+    assert qu(rows=0, epi=2) == gn.GN_OK and qu(rows=0, epi=2, x=None, q=None) == gn.GN_OK
+    assert qu(rows=1, epi=2) == gn.GN_ERR_UNSUPPORTED
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "silu", "gelu_tanh"])
+def test_activation_gradient_of_no_rows(gpu, act):
+    z = torch.zeros(0, 200, dtype=torch.bfloat16, device="cuda")
+    junk = torch.full((200,), 5.0, device="cuda")
+    del junk
+    q, s, qt, st, db = gn.act_grad_quant_fp8(z, z, epilogue=act)
+    assert q.shape == (0, 200) and s.shape == (0, 2) and qt.shape == (200, 0) and st.shape == (200, 0) and (db == 0).all()
+
+
 def test_helper_refusals(monkeypatch):
     monkeypatch.setattr(gn, "_on_gpu", lambda t: True)
     x = torch.zeros(4, 256, dtype=torch.bfloat16)

@@ -194,6 +194,31 @@ def test_widths_that_are_not_whole_16_bytes(gpu, M, N, K, norm, gemma, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("norm", ["none", "ln", "rms"])
+@pytest.mark.parametrize("N", [64, 300])
+def test_no_tokens(gpu, N, norm, act):
+    """A batch without tokens: empty y and dx, zeros for the parameters' gradients, by calls and by autograd."""
+    K = 136
+    t = odd_layer(0, N, K)
+    ng, nb = (None, None) if norm == "none" else (t["g"], t["beta"] if norm == "ln" else None)
+    args = dict(norm=norm, g=ng, beta=nb, eps=1e-5, act=act)
+    w = fl.prepare(t["W"])
+    junk = torch.full((N * K,), 5.0, device="cuda")  # what the allocator hands out next is not zero already
+    del junk
+    y, mean, rstd, z = fl.forward_keeping_z(t["x"], w, t["bias"], **args)
+    assert y.shape == z.shape == (0, N) and fl.forward(t["x"], w, t["bias"], **args)[0].shape == (0, N)
+    dx, dg, dbeta, dW, dbias = fl.backward(t["x"], w, z, t["dy"], mean=mean, rstd=rstd, **args)
+    assert dx.shape == (0, K) and dW.shape == (N, K) and dbias.shape == (N,)
+    assert all((v == 0).all() for v in (dW, dbias, dg, dbeta) if v is not None)
+    assert (dg is None) == (norm == "none") and (dbeta is None) == (norm != "ln")
+    x, W = (t[k].detach().requires_grad_(True) for k in ("x", "W"))
+    fl.Fp8LinearFunction.apply(x, W, t["bias"], ng, nb, norm, 1e-5, False, act).sum().backward()
+    assert x.grad.shape == (0, K) and (W.grad == 0).all()
+    assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
 def test_autograd_function_and_its_graph(gpu):
     """The autograd form gives the module's gradients; a second layer's captured forward and backward replay to the
     same bits while the first one's eager graph lives on (of other leaves: a capture of the same leaves' backward

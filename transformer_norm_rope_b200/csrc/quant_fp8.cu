@@ -971,7 +971,8 @@ extern "C" gn_status gn_quant_fp8(const void* x, const void* dy, void* q, float*
   if (rows < 0 || cols <= 0 || rows > 65535ll * kBlk || cols > INT32_MAX || ld_x < cols || (dy && ld_dy < cols)) return GN_ERR_SHAPE;
   if (q && (ld_q < cols || ld_s < blocks_of(cols))) return GN_ERR_SHAPE;
   if (qt && (ld_qt < rows || ld_st < blocks_of(rows))) return GN_ERR_SHAPE;
-  if ((tile && dy) || (!dy && epi != GN_EPI_NONE)) return GN_ERR_UNSUPPORTED;
+  // (a dy of no rows may well be a null pointer)
+  if ((tile && dy) || (!dy && rows > 0 && epi != GN_EPI_NONE)) return GN_ERR_UNSUPPORTED;
   cudaStream_t s = (cudaStream_t)stream;
   if (rows == 0) {
     if (db && cudaMemsetAsync(db, 0, (size_t)cols * 4, s) != cudaSuccess) return GN_ERR_CUDA;

@@ -99,8 +99,11 @@ def backward(x, weight: Weight, z, dy, norm: str = "none", g=None, beta=None, me
         xn, _ = gn.rmsnorm_fwd(x, g, eps, gemma=gemma, save_stats=False)
     else:
         xn = x
-    xt, xts = gn.quant_fp8(xn, by_rows=False, transposed=True)
-    dW = gn.linear_fp8(qt, st, xt, xts, out_dtype=torch.float32)
+    if x.shape[0] == 0:  # dW is a sum over no tokens
+        dW = torch.zeros((z.shape[1], x.shape[1]), dtype=torch.float32, device=x.device)
+    else:
+        xt, xts = gn.quant_fp8(xn, by_rows=False, transposed=True)
+        dW = gn.linear_fp8(qt, st, xt, xts, out_dtype=torch.float32)
     if norm == "ln":
         dx, dg, dbeta = gn.layernorm_bwd(x, g, beta, mean, rstd, dxn)
         return dx, dg, dbeta, dW, dbias
