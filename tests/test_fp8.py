@@ -376,6 +376,32 @@ def test_linear_row_scales_fp32(gpu, M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,N", [(1, 256), (16, 130), (30, 130), (60, 130), (128, 130), (300, 140), (2048, 2048)])
+def test_activations_keep_their_relative_precision(gpu, M, N, act):
+    """One product of ones a value, scaled to z: the activation of known z from -12 to 12, its small values on the
+    negative side included. Half a step of bf16; and for the evaluation z sigmoid(t) in fp32 with an exponential of
+    -t, t = z or 2 k (z + c z^3): 2^-22 (|t| + 4) of the value, t's own roundings and the functions' two ulps. A
+    sigmoid below 2^-126, the smallest normal number, is flushed to zero, and with it up to |z| 2^-126 of the value."""
+    code = torch.zeros(max(M, N), 128).to(F8).cuda()
+    code[:, 5] = torch.ones(()).to(F8).cuda()
+    if N > 1000:  # z = sa sb
+        sa, sb = torch.linspace(-12, 12, M, device="cuda")[:, None], torch.linspace(0.25, 1, blocks(N), device="cuda")[:, None]
+        z = sa.double() * sb.double().repeat_interleave(128, 0)[:N].t()
+        y = gn.linear_fp8(code[:M], sa, code[:N], sb, epilogue=act)
+    else:  # z = sa + d
+        sa, sb = torch.linspace(-6, 6, M, device="cuda")[:, None], torch.ones(blocks(N), 1, device="cuda")
+        d = torch.linspace(-6, 6, N, device="cuda")
+        z = (sa + d).double()  # one fp32 rounding, the kernel's own
+        y = gn.linear_fp8(code[:M], sa, code[:N], sb, d, epilogue=act)
+    t = z if act == "silu" else 2 * (2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3)
+    v = z * torch.sigmoid(t)
+    tol = (2.0 ** -8 + 2.0 ** -22 * (t.abs() + 4)) * v.abs() + 2.0 ** -126 * (1 + z.abs())
+    over = (y.double() - v).abs() - tol
+    assert (over <= 0).all(), f"{int((over > 0).sum())} of {over.numel()} off; worst relative {((y.double() - v).abs() / v.abs())[v.abs() > 1e-30].max():.3g}"
+
+
+@pytest.mark.gpu
 def test_linear_strides_and_neighbours(gpu):
     """Operands, scales and outputs that are parts of larger tensors; what lies around the output stays."""
     M, N, K = 150, 300, 500

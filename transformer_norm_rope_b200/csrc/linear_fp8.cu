@@ -140,17 +140,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
-// the activation of bf16 outputs, two values at a time: the hardware tanh, exponential and reciprocal
-template <int EPI>
-__device__ __forceinline__ float2 f8_act(float2 z) {
-  if constexpr (EPI == EPI_GELU_TANH) {
-    const float2 u = mul2(z, fma2(mul2(z, z), dup2(kGeluK * kGeluC), dup2(kGeluK))), h = mul2(z, dup2(0.5f));
-    return fma2(h, make_float2(tanh_f<true>(u.x), tanh_f<true>(u.y)), h);
-  } else {
-    return act_pair<EPI, true>(z);
-  }
-}
-
 // ---------------------------------------------------------------- pairs of SMs
 // Warp 0 loads (each CTA its 128 rows of A and its half of B's 256 rows per stage), warp 1 of the leader
 // issues the instructions, warps 4-11 of each CTA own 128 rows x 256 columns of totals: warp w the rows
@@ -424,7 +413,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
       if (!ok) break;
-      // bias, activation, and the way out: boxes of 128 bytes x 32 rows in shared memory (128-byte
+      // Bias and activation. (By act_pair: 1 + tanh(u) from the hardware tanh, which is off by 2^-11, left GeLU
+      // values near z = -3 off by a fifth. The exponential and reciprocal cost 2 % at 32768 x 5120 x 5120: 1000 us a
+      // call with the tanh, 1021 without.) Then the way out: boxes of 128 bytes x 32 rows in shared memory (128-byte
       // swizzle: 16-byte chunk c of row r at position c ^ (r % 8)), written by TMA with the rows and
       // columns past M and N clipped
       constexpr int kCols = F32 ? 32 : 64;  // columns of a box
@@ -453,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int cb = b * kCols + 8 * jj;  // column of the half
-                o[jj][i] = f8_act<EPI>(add2(acc[32 * (i >> 1) + 16 * (cb >> 6) + 2 * ((cb & 63) >> 3) + (i & 1)], d));
+                o[jj][i] = act_pair<EPI, true>(add2(acc[32 * (i >> 1) + 16 * (cb >> 6) + 2 * ((cb & 63) >> 3) + (i & 1)], d));
               }
             }
             box_free();
@@ -479,8 +470,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
               for (int e = 0; e < kE; e += 4) {
                 const float4 d = bias4(col0 + c * kE + e);
-                const float2 u = f8_act<EPI>(add2(acc[(b * kCols + c * kE + e) / 2], make_float2(d.x, d.y)));
-                const float2 v = f8_act<EPI>(add2(acc[(b * kCols + c * kE + e) / 2 + 1], make_float2(d.z, d.w)));
+                const float2 u = act_pair<EPI, true>(add2(acc[(b * kCols + c * kE + e) / 2], make_float2(d.x, d.y)));
+                const float2 v = act_pair<EPI, true>(add2(acc[(b * kCols + c * kE + e) / 2 + 1], make_float2(d.z, d.w)));
                 o[e] = u.x, o[e + 1] = u.y, o[e + 2] = v.x, o[e + 3] = v.y;
               }
               if constexpr (F32) w[c] = Vec<float>::pack(o);
@@ -567,7 +558,7 @@ __device__ __forceinline__ void add_totals(const Fp8Args& a, const float* total,
         if (j < cs) z[0] += v[u][j].x, z[1] += v[u][j].y, z[2] += v[u][j].z, z[3] += v[u][j].w;
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        const float2 o = f8_act<EPI>(make_float2(z[e] + d[e], z[e + 1] + d[e + 1]));
+        const float2 o = act_pair<EPI, true>(make_float2(z[e] + d[e], z[e + 1] + d[e + 1]));
         z[e] = o.x, z[e + 1] = o.y;
       }
       const int64_t at = (int64_t)(m0 + i + 4 * u) * a.ldy + n;
