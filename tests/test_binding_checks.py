@@ -185,3 +185,31 @@ def test_tiled_linear_chunk_bounds(rows, chunks):
         step256 = -(-(-(-rows // chunks)) // 256) * 256
         if -(-rows // step256) == len(b):
             assert all(r0 % 256 == 0 for r0, _ in b)
+
+
+@pytest.mark.parametrize("private", [True, False])
+def test_current_stream_for_any_false_value(monkeypatch, private):
+    """stream=None, 0 or False is the current stream, whether torch offers its raw handle or the public object only."""
+    class Current:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Current())
+    if private:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 74 + d, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert gn._stream() == gn._stream(None) == gn._stream(0) == gn._stream(False) == 77
+    assert gn._stream(type("S", (), {"cuda_stream": 5})()) == 5
+
+
+@pytest.mark.parametrize("stream", [None, 0, False])
+def test_helpers_of_streams_take_any_false_value(monkeypatch, stream):
+    seen = []
+
+    class Tensor:
+        is_cuda, device = True, torch.device("cuda", 0)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    gn._placed(lambda x, stream=None: seen.append(stream))(Tensor(), stream=stream)
+    assert seen == [stream]

@@ -162,10 +162,12 @@ def _ptr(t):
 
 
 def _stream(stream=None) -> int:
-    if stream is not None:
+    if stream:
         return stream.cuda_stream
     torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # the handle without a stream object around it, a microsecond less of a small call; torch may take it away
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
 
 
 def _epi(epi) -> int:
@@ -552,9 +554,9 @@ def _placed(f):
     @functools.wraps(f)
     def call(x, *args, stream=None, **kwargs):
         torch = _torch()
-        if not x.is_cuda or (stream is None and x.device.index == torch.cuda.current_device()):
+        if not x.is_cuda or (not stream and x.device.index == torch.cuda.current_device()):
             return f(x, *args, stream=stream, **kwargs)
-        if stream is None:
+        if not stream:
             with torch.cuda.device(x.device):
                 return f(x, *args, **kwargs)
         if stream.device != x.device:

@@ -1,7 +1,8 @@
 // act_pairs.cuh - the activations and their derivatives on pairs of values, to about 1e-6 of the value: for results
 // that keep more than the bf16 epilogues' hardware tanh (error 2^-11 of 1) carries - codes, whose rounding it would
-// move one time in a hundred, fp32 sums of gradients, and the small values on GeLU's negative side. FAST (bf16 inputs): the hardware's exponential and
-// reciprocal, two operations of the special-function unit a value; else the accurate forms.
+// move one time in a hundred, fp32 sums of gradients, and the small values on GeLU's negative side. FAST (bf16
+// inputs): the hardware's exponential and reciprocal, two operations of the special-function unit a value; else
+// the accurate forms.
 #pragma once
 
 #include "gn_common.cuh"
