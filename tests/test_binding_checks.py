@@ -213,3 +213,54 @@ def test_helpers_of_streams_take_any_false_value(monkeypatch, stream):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     gn._placed(lambda x, stream=None: seen.append(stream))(Tensor(), stream=stream)
     assert seen == [stream]
+
+
+def test_arguments_by_name_and_by_place(stub):
+    """Every argument of the GroupNorm and 8-bit helpers goes by name or by place, the first operand and the stream too."""
+    f8 = torch.float8_e4m3fn
+    x, st = z(2, 10, 64), z(2, 4, dtype=f32)
+    a, sa, sb = z(4, 128).to(f8), z(4, 1, dtype=f32), z(1, 1, dtype=f32)
+    gn.groupnorm_fwd(x=x, groups=4)
+    gn.groupnorm_fwd(x, 4, None, None, 1e-5, "none", None, True, None)
+    gn.groupnorm_bwd(x=x, groups=4, w=None, b=None, mean=st, rstd=st, dy=x)
+    gn.groupnorm_bwd(x, 4, None, None, st, st, x, "none", True, None)
+    gn.norm_quant_fp8(x=x)
+    gn.norm_quant_fp8(x, None, None, 1e-6, "rms", False, "none", True, None)
+    gn.quant_fp8(x=x[0])
+    gn.quant_fp8(x[0], False, True, False, None)
+    gn.act_grad_quant_fp8(z=x[0], dy=x[0])
+    gn.act_grad_quant_fp8(x[0], x[0], "silu", True, None)
+    gn.linear_fp8(a=a, sa=sa, b=a, sb=sb)
+    gn.linear_fp8(a, sa, a, sb, None, "none", None, None, False, None)
+    for f in (gn.groupnorm_fwd, gn.groupnorm_bwd, gn.norm_quant_fp8, gn.linear_fp8):
+        with pytest.raises(TypeError, match="missing"):
+            f()
+
+
+def test_the_stream_by_place_is_the_calls_stream(monkeypatch):
+    """... and its device is checked, and made current for the outputs, as for stream=."""
+    entered = []
+
+    class Stream:
+        def __init__(self, d):
+            self.device = torch.device("cuda", d)
+
+    class Tensor:
+        is_cuda, device = True, torch.device("cuda", 1)
+
+    class use:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            entered.append(self.s)
+
+        def __exit__(self, *exc):
+            pass
+
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    f = gn._placed(lambda x, groups, stream=None: stream)
+    own = Stream(1)
+    assert f(Tensor(), 4, own) is own and f(x=Tensor(), groups=4, stream=own) is own and entered == [own, own]
+    with pytest.raises(ValueError, match="the stream is on"):
+        f(Tensor(), 4, Stream(0))

@@ -551,18 +551,23 @@ def _placed(f):
     for the stream that the call uses: memory freed on one stream is otherwise handed out again
     while a kernel on another still works in it."""
 
+    names = tuple(inspect.signature(f).parameters)
+    at = names.index("stream")
+
     @functools.wraps(f)
-    def call(x, *args, stream=None, **kwargs):
-        torch = _torch()
-        if not x.is_cuda or (not stream and x.device.index == torch.cuda.current_device()):
-            return f(x, *args, stream=stream, **kwargs)
+    def call(*args, **kwargs):
+        x = args[0] if args else kwargs.get(names[0])
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        cuda = _torch().cuda
+        if not getattr(x, "is_cuda", False) or (not stream and x.device.index == cuda.current_device()):
+            return f(*args, **kwargs)
         if not stream:
-            with torch.cuda.device(x.device):
-                return f(x, *args, **kwargs)
+            with cuda.device(x.device):
+                return f(*args, **kwargs)
         if stream.device != x.device:
             raise ValueError(f"the stream is on {stream.device}, the operands on {x.device}")
-        with torch.cuda.stream(stream):
-            return f(x, *args, stream=stream, **kwargs)
+        with cuda.stream(stream):
+            return f(*args, **kwargs)
 
     return call
 
