@@ -194,6 +194,78 @@ def test_widths_that_are_not_whole_16_bytes(gpu, M, N, K, norm, gemma, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "silu", "gelu_tanh"])
+@pytest.mark.parametrize("norm,gemma", [("none", False), ("ln", False), ("rms", False), ("rms", True)])
+@pytest.mark.parametrize("M,N,K", [(37, 136, 264), (300, 520, 648), (1030, 2056, 1304)])
+def test_gradients_on_the_layers_own_codes(gpu, M, N, K, norm, gemma, act):
+    t = layer(M, N, K)
+    ng, nb = (None, None) if norm == "none" else (t["g"], t["beta"] if norm == "ln" else None)
+    args = dict(norm=norm, g=ng, beta=nb, eps=1e-5, gemma=gemma, act=act)
+    w = fl.prepare(t["W"])
+    _, mean, rstd, z = fl.forward_keeping_z(t["x"], w, t["bias"], **args)
+    check_gradients(t, w, z, t["dy"], mean, rstd, fl.backward(t["x"], w, z, t["dy"], mean=mean, rstd=rstd, **args), norm, gemma, act)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,d1,d2,d3", [("silu", 1.1, 0.5, 0.309), ("gelu_tanh", 1.13, 0.798, 0.777)])
+def test_bias_gradient_against_differences(gpu, act, d1, d2, d3):
+    """Central differences of f(bias) = sum(y dy) through the layer itself, along v = sign(dbias), where the derivative
+    sum |dbias| is at its largest. Off by at most (d1 to d3: the largest slope, curvature and third derivative):
+    * the rounding of each y to bf16, 2^-8 |y| <= 2^-8 (|y0| + d1 h), over h: sum |dy| of it;
+    * the third order, h^2 / 6 d3 sum |dy|;
+    * dbias comes from z rounded to bf16: d2 2^-8 |z| sum |dy|; and 1 % of all that for fp32 sums.
+    A bias gradient of zeros must not pass."""
+    M, N, K, h = 16, 256, 512, 0.25
+    t = layer(M, N, K, seed=3)
+    w = fl.prepare(t["W"])
+    dy = t["dy"].double()
+    f = lambda d: (fl.forward(t["x"], w, d, act=act)[0].double() * dy).sum()  # noqa: E731
+    y, _, _, z = fl.forward_keeping_z(t["x"], w, t["bias"], act=act)
+    dbias = fl.backward(t["x"], w, z, t["dy"], act=act)[4].double()
+    v = dbias.sign().float()
+    num = (f(t["bias"] + h * v) - f(t["bias"] - h * v)) / (2 * h)
+    ana = dbias.abs().sum()
+    off = 2.0 ** -8 * (y.double().abs() + d1 * h) / h + h * h / 6 * d3 + d2 * 2.0 ** -8 * z.double().abs()
+    tol = 1.01 * (off * dy.abs()).sum()
+    assert tol <= 0.25 * num.abs(), f"the tolerance {tol:.3g} says nothing about {num:.3g}"
+    assert (num - ana).abs() <= tol
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,d1,d2,d3", [("none", 1.0, 0.0, 0.0), ("silu", 1.1, 0.5, 0.309), ("gelu_tanh", 1.13, 0.798, 0.777)])
+def test_weight_gradient_against_differences(gpu, act, d1, d2, d3):
+    """Central differences through the layer itself as the scales of W's 128 x 128 blocks move by 1 +- h, each block in
+    the direction that adds to f = sum(y dy): W's values move along V, its blocks times their directions, and z with
+    them by exactly h zV, zV = x V^T (its codes are those of x). The derivative is sum(dW V). Off by
+    * at most, as for the bias: (2^-8 (|y| + d1 h |zV|) / h + h^2 / 6 d3 |zV|^3) |dy| and d2 2^-8 |z zV dy|, summed;
+    * the codes of dz and x in dW, half a step 2^-4 of each of dW's terms, two operands: independent roundings, so four
+      times the 2-norm of the terms |dz x V|, 2^-4 sqrt(2 / 3) each (a rounding's spread is its half step over sqrt 3).
+    A weight gradient of zeros must not pass."""
+    M, N, K, h = 2, 512, 640, 0.125
+    t = layer(M, N, K, seed=5)
+    w = fl.prepare(t["W"])
+    dy = t["dy"].double()
+    y, _, _, z = fl.forward_keeping_z(t["x"], w, t["bias"], act=act)
+    dW = fl.backward(t["x"], w, z, t["dy"], act=act)[3].double()
+    W = values(w.q, w.scale, tile=True)
+    per_block = (dW * W).reshape(N // 128, 128, K // 128, 128).sum((1, 3))
+    c = per_block.sign()
+    V = W * c.repeat_interleave(128, 0).repeat_interleave(128, 1)
+    f = lambda k: (fl.forward(t["x"], w._replace(scale=w.scale * (1 + k * c).float()), t["bias"], act=act)[0].double() * dy).sum()  # noqa: E731
+    num, ana = (f(h) - f(-h)) / (2 * h), per_block.abs().sum()
+    q, s, _, _ = gn.norm_quant_fp8(t["x"], norm="none")
+    x = values(q, s)
+    zV = x @ V.t()
+    off = (2.0 ** -8 * (y.double().abs() + d1 * h * zV.abs()) / h + h * h / 6 * d3 * zV.abs() ** 3 + d2 * 2.0 ** -8 * (z.double() * zV).abs())
+    zz = z.double().clone().requires_grad_(True)
+    (dz,) = torch.autograd.grad((act64(zz, act) * dy).sum(), zz)
+    codes = 4 * 2.0 ** -4 * (2 / 3) ** 0.5 * (dz.square() * (x.square() @ V.square().t())).sum().sqrt()
+    tol = 1.01 * (off * dy.abs()).sum() + codes
+    assert tol <= 0.4 * num.abs(), f"the tolerance {tol:.3g} says nothing about {num:.3g}"
+    assert (num - ana).abs() <= tol
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["none", "silu"])
 @pytest.mark.parametrize("norm", ["none", "ln", "rms"])
 @pytest.mark.parametrize("N", [64, 300])
