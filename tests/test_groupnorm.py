@@ -113,6 +113,42 @@ def test_groupnorm(gpu, N, S, C, G, dt, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("N,S,C,G", [(1, 63, 320, 32), (2, 50, 40, 1), (2, 65, 77, 7), (1, 4099, 128, 32), (2, 1031, 640, 32), (3, 2500, 1032, 2), (2, 9000, 520, 1)])
+def test_activations_of_bf16_images_are_evaluated_in_fp32(gpu, N, S, C, G, act):
+    """Half a step of bf16 and fp32 evaluation, nothing coarser, on chip and in two passes. With t = z (SiLU) or
+    2 k (z + c z^3) (GeLU), p = sigmoid(t) and q = 1 - p:
+    * y = z p: 2^-22 (|t| + 4) of the value for the exponential's argument and the functions' ulps; z's own
+      2e-6 (|z| + |b| + 1), as in check(), times the largest slope, 1.13;
+    * act' = p (1 + z q t'): the same relative part of each of its two terms, and z's error times the largest
+      curvature, 0.8: e, which reaches dx, dw and db times dy and what multiplies it there; their sums and the
+      rest as in check().
+    An activation that is off by 2^-11 of 1 must not pass."""
+    t = make(N, S, C, "bf16", ld=(C + 7) // 8 * 8)
+    ref, wd, bd = reference(t, G, 1e-5, act)
+    y, mean, rstd = gn.groupnorm_fwd(t["x"], G, t["w"], t["b"], epilogue=act)
+    dx, dw, db = gn.groupnorm_bwd(t["x"], G, t["w"], t["b"], mean, rstd, t["dy"], epilogue=act)
+    z, dy, xh, s = ref["z"], t["dy"].double().abs(), ref["xhat"].abs(), ref["rstd"].repeat_interleave(C // G, dim=-1)[:, None, :]
+    k = (2 / torch.pi) ** 0.5
+    u, du = (z, torch.ones_like(z)) if act == "silu" else (2 * k * (z + 0.044715 * z ** 3), 2 * k * (1 + 3 * 0.044715 * z ** 2))
+    p = torch.sigmoid(u)
+    ez, rel = 2e-6 * (z.abs() + bd.abs() + 1), 2.0 ** -22 * (u.abs() + 4)
+    y_tol = 2.0 ** -8 * ref["y"].abs() + rel * ref["y"].abs() + 1.13 * ez
+    within(y, ref["y"], y_tol, "y")
+    coarse = z * (p + 2.0 ** -12)  # (1 + tanh) / 2 with the hardware tanh's error
+    assert ((coarse - ref["y"]).abs() > y_tol).any()
+
+    e = (rel * (p + (z * p * (1 - p) * du).abs()) + 0.8 * ez) * dy  # of g = dy act'
+    group = lambda v: v.reshape(N, S, G, -1).mean(dim=(1, 3)).repeat_interleave(C // G, dim=-1)[:, None, :]  # noqa: E731
+    gw, ew = ref["g"].abs() * wd.abs(), e * wd.abs()
+    through = lambda v: s * (v + group(v) + xh * group(v * xh))  # noqa: E731
+    within(dx, ref["dx"], 2.0 ** -8 * ref["dx"].abs() + 8e-6 * through(gw) + through(ew), "dx")
+    within(dw, ref["dw"], ((4e-6 * ref["g"].abs() + e) * xh).sum((0, 1)) + 1e-6, "dw")
+    within(db, ref["db"], (4e-6 * ref["g"].abs() + e).sum((0, 1)) + 1e-6, "db")
+    assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["none", "silu"])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("C,G", [(171, 1), (77, 7), (5, 5), (4104, 27), (1, 1)])
