@@ -266,6 +266,31 @@ def test_weight_gradient_against_differences(gpu, act, d1, d2, d3):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt,K", [("bf16", 16384), ("bf16", 16392), ("bf16", 20480), ("f32", 8192), ("f32", 8196), ("f32", 20480)])
+@pytest.mark.parametrize("M", [3, 140])
+def test_rows_wider_than_a_norm_takes(gpu, M, K, dt):
+    """Without a norm in front any width is taken, forward and (bf16) backward; with one a row is at most 32 KiB."""
+    N = 72
+    t = odd_layer(M, N, K)  # (8196 bf16 values are not whole 16 bytes)
+    x = t["x"] if dt == "bf16" else t["x"].float()
+    w = fl.prepare(t["W"])
+    y, mean, rstd = fl.forward(x, w, t["bias"])
+    q, s = gn.quant_fp8(x)
+    a, b = values(q, s), values(w.q, w.scale, tile=True)
+    v = a @ b.t() + t["bias"].double()
+    tol = 2.0 ** -8 * v.abs() + 2.0 ** -24 * (K + K / 128 + 5) * (a.abs() @ b.abs().t() + t["bias"].double().abs())
+    assert mean is None and rstd is None and ((y.double() - v).abs() <= tol).all()
+    if dt == "bf16":
+        _, _, _, z = fl.forward_keeping_z(x, w, t["bias"])
+        check_gradients(t, w, z, t["dy"], None, None, fl.backward(x, w, z, t["dy"]), "none", False, "none")
+    if K * x.element_size() > 32768:
+        with pytest.raises(gn.GnError) as e:
+            fl.forward(x, w, norm="ln")
+        assert e.value.status == gn.GN_ERR_UNSUPPORTED
+    assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["none", "silu"])
 @pytest.mark.parametrize("norm", ["none", "ln", "rms"])
 @pytest.mark.parametrize("N", [64, 300])

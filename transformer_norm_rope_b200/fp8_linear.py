@@ -65,10 +65,13 @@ def _whole_rows(t):
 def forward(x, weight: Weight, bias=None, norm: str = "none", g=None, beta=None, eps: float = 1e-5, gemma: bool = False,
             act: str = "none"):
     """y [M, N] bf16 = act(norm(x) W^T + bias) for x [M, K] (bf16 or, without a backward, fp32; bias fp32 [N])
-    -> (y, mean or None, rstd or None)."""
+    -> (y, mean or None, rstd or None). Rows of at most 32 KiB behind a norm, of any width without one."""
     if x.dim() != 2:
         raise ValueError(f"x {tuple(x.shape)} must be [M, K]: take its rows together")
-    q, s, mean, rstd = gn.norm_quant_fp8(x, g, beta, eps, norm=norm, gemma=gemma)
+    if norm == "none" and x.shape[1] * x.element_size() > 32768:  # no statistics, so any width: the same codes by tiles
+        (q, s), mean, rstd = gn.quant_fp8(x), None, None
+    else:
+        q, s, mean, rstd = gn.norm_quant_fp8(x, g, beta, eps, norm=norm, gemma=gemma)
     return gn.linear_fp8(q, s, weight.q, weight.scale, bias, epilogue=act), mean, rstd
 
 
