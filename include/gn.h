@@ -324,10 +324,11 @@ gn_status gn_act_fwd(const void* z, void* y, int64_t n, gn_epilogue epi, gn_dtyp
  *   y = epi((x - mu) s w_c + b_c)
  *   mean[n, group] = mu, rstd[n, group] = s                (fp32 [N, G]; each may be NULL)
  * w, b: dt [C]; w == NULL means 1, b == NULL means 0. x, y: 16-byte aligned, row strides of whole
- * 16 bytes; any C, G dividing C. y may alias x when ld_y == ld_x (in place).
+ * 16 bytes; any C, G dividing C, N and C at most 2^20. y may alias x when ld_y == ld_x (in place).
  * ws: device scratch of gn_groupnorm_fwd_workspace(N, S, C, G, dt) bytes, 16-byte aligned, owned by
  * the caller, contents ignored on entry; calls that overlap on the GPU need one each. The size is
- * that of the current device; 0 for images that stay on chip: ws may then be NULL. Every sum runs in a fixed order: the same bits on every run.
+ * that of the current device; 0 for images that stay on chip: ws may then be NULL. Every sum runs in
+ * a fixed order: the same bits on every run.
  * N == 0 or S == 0: nothing is launched and no statistic is written.
  * Errors: GN_ERR_DTYPE, GN_ERR_SHAPE (sizes, G not dividing C, strides), GN_ERR_NULL, GN_ERR_ALIGN,
  * GN_ERR_WORKSPACE, GN_ERR_CUDA. */
