@@ -138,6 +138,37 @@ def test_norm_quant_rows_whose_beginning_is_far_off(gpu, dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shift", [0.0, 300.0])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,hidden", [(1200, 5120), (1200, 2056), (1200, 4096)])
+def test_norm_quant_means_are_rounded_once(gpu, rows, hidden, dt, shift):
+    """LayerNorm's mean of rows with mean in [1, 2) and unit spread, also where the row's first part lies far off. Root
+    mean square error over the rows, in 2^-24 (half an ulp of the mean; the last rounding alone leaves 0.58):
+    * bf16 rows: x - K and its sums have few bits and are all but exact: 1, and 4 next to values of 300;
+    * fp32 rows summed as x - K (up to 4096 wide): n independent roundings of partial sums p, sqrt(n) p / (sqrt 3 n): 0.4
+      for p = 30, so 1; with four values of 301 in a partial sum that times 1206 / 30;
+    * wider ones, summed as they are: 1, 2, 4 ... roundings of sums P, P / 2, P / 4 ...: sqrt(2 / 3) P / n, P / n = 1.5
+      (256 x 301 / n next to 300), with the last rounding sqrt(0.58^2 + 1.22^2) = 1.35.
+    (Roundings that are the same for all values of a row would not stay so small.)"""
+    g = torch.Generator().manual_seed(rows + hidden)
+    x = torch.randn(rows, hidden, generator=g) + 1.5
+    if shift:  # first values up, the last down by as much: the mean stays
+        x[:, :256] += shift
+        x[:, -256:] -= shift
+    x = padded(x, DT[dt])
+    _, _, mean, _ = gn.norm_quant_fp8(x, norm="ln", eps=1e-5)
+    mu = x.double().mean(1)
+    err = (mean.double() - mu).square().mean().sqrt()
+    if dt == "bf16":
+        tol = 4 if shift else 1
+    elif hidden <= 4096:
+        tol = 1 + hidden ** -0.5 * 1206 / 3 ** 0.5 if shift else 1
+    else:
+        tol = 0.58 + (2 / 3) ** 0.5 * 256 * 301.5 / hidden if shift else 1.35
+    assert err <= 2.0 ** -24 * tol, f"{err * 2 ** 24:.3g}, {tol:.3g} allowed"
+
+
+@pytest.mark.gpu
 def test_norm_quant_parameters_off_16_bytes(gpu):
     x = torch.randn(9, 520, device="cuda").bfloat16()
     w, b = (torch.randn(523, device="cuda").bfloat16() for _ in range(2))
