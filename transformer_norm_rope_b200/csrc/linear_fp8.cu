@@ -417,9 +417,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!ok) break;
       // Bias and activation. (By act_pair: 1 + tanh(u) from the hardware tanh, which is off by 2^-11, left GeLU
       // values near z = -3 off by a fifth. 32768 x 5120 x 5120: 995 us with the tanh, 1013 with these; a tile's
-      // work outside its blocks 5.8 us and 6.3, without an activation 3.5.) Then the way out: boxes of 128 bytes x 32 rows in shared memory (128-byte
-      // swizzle: 16-byte chunk c of row r at position c ^ (r % 8)), written by TMA with the rows and
-      // columns past M and N clipped
+      // work outside its blocks 5.8 us and 6.3, without an activation 3.5.) Then the way out: boxes of 128 bytes x
+      // 32 rows in shared memory (128-byte swizzle: 16-byte chunk c of row r at position c ^ (r % 8)), written by
+      // TMA with the rows and columns past M and N clipped
       constexpr int kCols = F32 ? 32 : 64;  // columns of a box
 #pragma unroll
       for (int b = 0; b < 128 / kCols; ++b) {
