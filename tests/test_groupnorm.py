@@ -113,6 +113,33 @@ def test_groupnorm(gpu, N, S, C, G, dt, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("spread", [2.0, 30.0])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N,S,C,G", [(15, 1017, 3, 3), (13, 179, 9, 9), (40, 1017, 5, 1), (20, 5000, 9, 9), (30, 6000, 3, 1), (8, 3156, 42, 6), (4, 9000, 264, 24)])
+def test_statistics_of_narrow_images(gpu, N, S, C, G, dt, spread):
+    """Few channels put many threads on each: their join must not round the mean once a thread. 2-norms over the groups,
+    in u = 2^-24, independent roundings (uniform, 0.58 u each) adding up in squares:
+    * mean: the threads' (averaged), the slab's, the products and the tree of the join (with halves of its sums: 0.82
+      together), the division: 1.3 u of |mu|, and as much of sigma for the deviations: 2 u (|mu| + sigma) allowed;
+    * rstd: half of the variance's few u, the root and the division: 3 u;
+    * y (fp32): the mean's error times rstd and w, and the rounding of (x - mu), of its product, of w and of the sum."""
+    t = make(N, S, C, dt, ld=(C + 7) // 8 * 8, spread=spread, seed=3)
+    ref, wd, bd = reference(t, G, 1e-5, "none")
+    y, mean, rstd = gn.groupnorm_fwd(t["x"], G, t["w"], t["b"])
+    u = 2.0 ** -24
+    off = lambda got, v: (got.double() - v).norm()  # noqa: E731
+    em = 2 * u * (ref["mean"].abs() + 1 / ref["rstd"])
+    assert off(mean, ref["mean"]) <= em.norm(), f"mean: {off(mean, ref['mean']) / ref['mean'].norm() / u:.3g} u"
+    assert off(rstd, ref["rstd"]) <= 3 * u * ref["rstd"].norm(), f"rstd: {off(rstd, ref['rstd']) / ref['rstd'].norm() / u:.3g} u"
+    if dt == "f32":
+        rep = lambda v: v.repeat_interleave(C // G, dim=-1)[:, None, :]  # noqa: E731
+        tol = ((rep(em * ref["rstd"]) + 3 * 0.58 * u * ref["xhat"].abs()) * wd.abs() + 0.58 * u * ref["y"].abs()
+               + 3 * u * ref["xhat"].abs() * wd.abs())  # the last term: rstd's
+        assert off(y, ref["y"]) <= tol.norm(), f"y: {off(y, ref['y']) / ref['y'].norm() / u:.3g} u"
+    assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 @pytest.mark.parametrize("N,S,C,G", [(1, 63, 320, 32), (2, 50, 40, 1), (2, 65, 77, 7), (1, 4099, 128, 32), (2, 1031, 640, 32), (3, 2500, 1032, 2), (2, 9000, 520, 1)])
 def test_activations_of_bf16_images_are_evaluated_in_fp32(gpu, N, S, C, G, act):

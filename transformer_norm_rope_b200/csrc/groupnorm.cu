@@ -16,7 +16,7 @@
 // in the backward the channels of a group), and an elementwise pass. A thread keeps one 16-byte vector of channels and
 // walks down the positions, so its per-channel sums and parameters stay in registers and every warp
 // access covers whole runs of a row. The forward's sums are (mean, centred sum of squares) per
-// channel, taken around a value of the slab and joined with Chan's update: no E[x^2] - E[x]^2 cancellation.
+// channel, taken around a value of the slab and joined as deviations from a mean: no E[x^2] - E[x]^2 cancellation.
 #include <type_traits>
 
 #include "act_pairs.cuh"
@@ -239,24 +239,38 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm<T>) gn_stats_kernel(const 
   for (int e = 0; e < E; ++e) sm_mean[threadIdx.x * E + e] = mean[e], sm_m2[threadIdx.x * E + e] = m2[e];
   sm_cnt[threadIdx.x] = cnt;
   __syncthreads();
-  // channel j of the tile: merge the rl threads that hold it, in order
+  // channel j of the tile: as many lanes as there are to spare join the rl threads that hold it, as deviations from the first
+  // one's mean (always there): mean = m0 + d, d = sum n_k (m_k - m0) / n; squares = sum of theirs + n_k (m_k - m0 - d)^2.
+  // One rounding of the mean's size is left. (Merged one after the other, every step rounded the mean and the squares:
+  // with 256 threads a channel the means of 15 x 1017 x 3 fp32 were off by 2.9e-7 of them, 6.6e-8 by an elementary sum.)
+  const float rows = (float)(p.r1 - p.r0);
   float* ch_mean = sm_cnt + kThreads;
   float* ch_m2 = ch_mean + g.tv * E;
   const int tile = blockIdx.x % g.tiles, c_lo = tile * g.tv * E;
   const int nch = g.C - c_lo < g.tv * E ? g.C - c_lo : g.tv * E;
-  for (int j = threadIdx.x; j < nch; j += kThreads) {
-    float mu = 0.0f, q = 0.0f, n = 0.0f;
-    for (int k = 0; k < g.rl; ++k) {
-      const int t = k * g.tv + j / E;
-      const float nk = sm_cnt[t];
-      if (nk == 0.0f) continue;
-      const float tot = n + nk, dl = sm_mean[t * E + j % E] - mu;
-      mu = fmaf(dl, nk / tot, mu);
-      q += fmaf(dl * dl, n * (nk / tot), sm_m2[t * E + j % E]);
-      n = tot;
+  int share = 1;
+  while (share < 32 && share * 2 * g.tv * E <= kThreads) share *= 2;
+  auto lanes_sum = [&](float v) {
+    for (int o = share / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  for (int j0 = 0; j0 < nch; j0 += kThreads / share) {  // the same number of turns for every lane
+    const int j = j0 + threadIdx.x / share, jc = j < nch ? j : nch - 1;
+    const int first = (int)threadIdx.x & (share - 1);
+    const float *mk = sm_mean + jc, *qk = sm_m2 + jc, *ck = sm_cnt + jc / E;  // thread k g.tv + jc / E, its value jc % E
+    const float m0 = *mk;
+    float d = 0.0f, q = 0.0f;
+    for (int k = first; k < g.rl; k += share) {
+      const float nk = ck[k * g.tv];
+      if (nk > 0.0f) d = fmaf(nk, mk[k * g.tv * E] - m0, d);
     }
-    ch_mean[j] = mu;
-    ch_m2[j] = q;
+    d = lanes_sum(d) / rows;
+    for (int k = first; k < g.rl; k += share) {
+      const float nk = ck[k * g.tv], dl = mk[k * g.tv * E] - m0 - d;
+      if (nk > 0.0f) q += fmaf(nk * dl, dl, qk[k * g.tv * E]);
+    }
+    q = lanes_sum(q);
+    if (first == 0 && j < nch) ch_mean[j] = m0 + d, ch_m2[j] = q;
   }
   __syncthreads();
   // the tile's part of each group: as many neighbouring lanes as it has channels, a warp at most
@@ -264,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm<T>) gn_stats_kernel(const 
   int team = 32;
   while (team > 1 && team / 2 >= g.P) team /= 2;
   const int lane = threadIdx.x & (team - 1), per = kThreads / team;
-  const float rows = (float)(p.r1 - p.r0);
   auto team_sum = [&](float v) {
     for (int d = team / 2; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
