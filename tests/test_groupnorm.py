@@ -140,6 +140,26 @@ def test_statistics_of_narrow_images(gpu, N, S, C, G, dt, spread):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N,S,C,G", [(15, 1017, 3, 3), (13, 179, 9, 9), (8, 50000, 3, 3), (2, 30000, 40, 8), (8, 3156, 42, 6), (4, 9000, 264, 24), (1, 60000, 24, 24)])
+def test_parameter_gradients_of_narrow_images(gpu, N, S, C, G, dt):
+    """dw and db are sums over all positions: no part of them may be a long chain. Against the same formula in 64 bits on
+    the saved statistics, 2-norms over the channels, in u = 2^-24 of the 2-norm of a channel's terms. A chain of K
+    roundings of growing partial sums of independent terms leaves 0.58 sqrt(K / 2), a tree of L levels 0.58 sqrt(L): a
+    thread's positions (under 30 here: 2.2), a lane's threads (16: 1.6), lanes (5 levels: 1.3), slabs (a chain of 8 and 7
+    levels: 1.9), images (a chain of 15: 1.6), x^ and its product (1): 4.1 in squares; 6 allowed."""
+    t = make(N, S, C, dt, ld=(C + 7) // 8 * 8, seed=5)
+    _, mean, rstd = gn.groupnorm_fwd(t["x"], G, t["w"], t["b"])
+    _, dw, db = gn.groupnorm_bwd(t["x"], G, t["w"], t["b"], mean, rstd, t["dy"])
+    rep = lambda v: v.double().repeat_interleave(C // G, dim=-1)[:, None, :]  # noqa: E731
+    dy, xh = t["dy"].double(), (t["x"].double() - rep(mean)) * rep(rstd)
+    for got, terms, what in ((db, dy, "db"), (dw, dy * xh, "dw")):
+        off = (got.double() - terms.sum((0, 1))).norm() / terms.square().sum((0, 1)).sqrt().norm() * 2 ** 24
+        assert off <= 6, f"{what}: {off:.3g} u"
+    assert gpu.device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 @pytest.mark.parametrize("N,S,C,G", [(1, 63, 320, 32), (2, 50, 40, 1), (2, 65, 77, 7), (1, 4099, 128, 32), (2, 1031, 640, 32), (3, 2500, 1032, 2), (2, 9000, 520, 1)])
 def test_activations_of_bf16_images_are_evaluated_in_fp32(gpu, N, S, C, G, act):

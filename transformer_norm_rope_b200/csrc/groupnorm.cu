@@ -169,6 +169,17 @@ __device__ __forceinline__ void store_packed(T* row, const Place& p, int C, cons
   }
 }
 
+// lanes of a warp that can share one of n columns, a power of two; the sum over them (in every lane)
+__device__ __forceinline__ int spare_lanes(int n) {
+  int l = 1;
+  while (l < 32 && l * 2 * n <= kThreads) l *= 2;
+  return l;
+}
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+  for (int o = lanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 // ---------------------------------------------------------------- forward: slab statistics
 // part[n][chunk][slot] = (mean, centred sum of squares) over the slab of the channels that a group has in a
 // column tile; slot = tile + group (neighbouring tiles share at most one group).
@@ -248,12 +259,7 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm<T>) gn_stats_kernel(const 
   float* ch_m2 = ch_mean + g.tv * E;
   const int tile = blockIdx.x % g.tiles, c_lo = tile * g.tv * E;
   const int nch = g.C - c_lo < g.tv * E ? g.C - c_lo : g.tv * E;
-  int share = 1;
-  while (share < 32 && share * 2 * g.tv * E <= kThreads) share *= 2;
-  auto lanes_sum = [&](float v) {
-    for (int o = share / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  };
+  const int share = spare_lanes(g.tv * E);
   for (int j0 = 0; j0 < nch; j0 += kThreads / share) {  // the same number of turns for every lane
     const int j = j0 + threadIdx.x / share, jc = j < nch ? j : nch - 1;
     const int first = (int)threadIdx.x & (share - 1);
@@ -264,12 +270,12 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm<T>) gn_stats_kernel(const 
       const float nk = ck[k * g.tv];
       if (nk > 0.0f) d = fmaf(nk, mk[k * g.tv * E] - m0, d);
     }
-    d = lanes_sum(d) / rows;
+    d = lanes_sum(d, share) / rows;
     for (int k = first; k < g.rl; k += share) {
       const float nk = ck[k * g.tv], dl = mk[k * g.tv * E] - m0 - d;
       if (nk > 0.0f) q += fmaf(nk * dl, dl, qk[k * g.tv * E]);
     }
-    q = lanes_sum(q);
+    q = lanes_sum(q, share);
     if (first == 0 && j < nch) ch_mean[j] = m0 + d, ch_m2[j] = q;
   }
   __syncthreads();
@@ -488,15 +494,20 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm<T>) gn_bwd_sums_kernel(con
 #pragma unroll
   for (int e = 0; e < E; ++e) sm_a[threadIdx.x * E + e] = A[e], sm_b[threadIdx.x * E + e] = B[e];
   __syncthreads();
-  for (int j = threadIdx.x; j < g.tv * E; j += kThreads) {
-    const int c = (blockIdx.x % g.tiles) * g.tv * E + j;
-    if (c >= g.C) continue;
+  // as many lanes as there are to spare share the sum over the rl threads of a channel: parts of at most 16 and a tree
+  // (one after the other, 256 of them, dw and db of narrow images had up to four times an elementary sum's error)
+  const int share = spare_lanes(g.tv * E), lane = (int)threadIdx.x & (share - 1);
+  const int c0 = (blockIdx.x % g.tiles) * g.tv * E, nch = g.C - c0 < g.tv * E ? g.C - c0 : g.tv * E;
+  float2* out = part + ((int64_t)p.n * g.chunks + p.chunk) * g.C + c0;
+  for (int j0 = 0; j0 < nch; j0 += kThreads / share) {  // the same number of turns for every lane
+    const int j = j0 + (int)threadIdx.x / share, jc = j < nch ? j : nch - 1;
     float ta = 0.0f, tb = 0.0f;
-    for (int k = 0; k < g.rl; ++k) {
-      ta += sm_a[k * g.tv * E + j];
-      tb += sm_b[k * g.tv * E + j];
+    for (int k = lane; k < g.rl; k += share) {
+      ta += sm_a[k * g.tv * E + jc];
+      tb += sm_b[k * g.tv * E + jc];
     }
-    part[((int64_t)p.n * g.chunks + p.chunk) * g.C + c] = make_float2(ta, tb);
+    if (share > 1) ta = lanes_sum(ta, share), tb = lanes_sum(tb, share);
+    if (lane == 0 && j < nch) out[j] = make_float2(ta, tb);
   }
 }
 
@@ -536,6 +547,8 @@ __global__ void __launch_bounds__(kJoin) gn_bwd_join_kernel(const float2* __rest
   const int n = blockIdx.x / g.G, gr = blockIdx.x % g.G;
   float m1 = 0.0f, m2 = 0.0f;
   const int parts = g.P < kJoin ? kJoin / g.P : 1;
+  int tree = 0;  // the largest power of two below the parts that hold slabs
+  for (int h = 1; h < parts && h < g.chunks; h *= 2) tree = h;
   for (int b0 = 0; b0 < g.P; b0 += kJoin) {  // a thread: every `parts`-th slab of one channel
     const int j = g.P < kJoin ? (int)threadIdx.x % g.P : b0 + (int)threadIdx.x;
     const int k0 = g.P < kJoin ? (int)threadIdx.x / g.P : 0;
@@ -547,8 +560,11 @@ __global__ void __launch_bounds__(kJoin) gn_bwd_join_kernel(const float2* __rest
     }
     sums[threadIdx.x] = t;
     __syncthreads();
+    for (int h = tree; h > 0; h /= 2) {  // the parts as a tree: place k gets k + h
+      if (k0 < h && k0 + h < parts) t = add2(t, sums[(k0 + h) * g.P + j]), sums[k0 * g.P + j] = t;
+      __syncthreads();
+    }
     if (j < g.P && k0 == 0) {
-      for (int k = 1; k < parts; ++k) t = add2(t, sums[k * g.P + j]);
       const int c = gr * g.P + j;
       chan[(int64_t)n * 2 * g.C + c] = t.y;
       chan[(int64_t)n * 2 * g.C + g.C + c] = t.x;
