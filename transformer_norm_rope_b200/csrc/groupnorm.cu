@@ -1150,7 +1150,7 @@ Bundle plan_resident(int64_t N, int64_t S, int64_t C, int64_t G, int es, int mos
   auto fits = [&](int64_t v, int64_t cs) { return v <= kResThreads && (S + cs - 1) / cs <= (kResThreads / v) * (int64_t)most; };
   // beyond 4 MiB in all, only images of which a block holds a bundle by itself, a few vectors a thread: else
   // the two passes, whose many short-lived loads keep memory busier, are faster (2 x 4096 x 640 bf16 forward: 27
-  // us on chip, 17 in two passes; 2 x 1024 x 640: 8 and 13). The backward goes by the same bytes of x, though it holds
+  // us on chip, 19 in two passes; 2 x 1024 x 640: 8 and 13). The backward goes by the same bytes of x, though it holds
   // dy as well: 2 x 1024 x 640 13.3 on chip and 16.3, 1 x 4096 x 512 18.5 and 17.6, 4 x 1024 x 640 25.7 and 19.5; where
   // one block holds a bundle it errs, by 3 us in 23 at 8 x 256 x 1280
   if (!fits(bv, 8) || (N * S * C * es > (4 << 20) && S > (kResThreads / bv) * 4)) return g;
